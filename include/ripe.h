@@ -114,6 +114,29 @@ typedef struct ripe_stats {
 int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_dim, int loops,
                      int window, int max_T, int max_B, int window_mode, ripe_cache_t **out);
 
+/*
+ * ripe_cache_alloc with the deepest-plane region in 8 bits, for long contexts, where streaming that
+ * region is the cost of a verification.  Arguments and errors as there; every call on a cache takes
+ * either kind.  (The pages have no counterpart: 8-bit key/value caches are common practice.)
+ *   Blocks of 64 positions of one layer, sequence and kv head, K and V apart, hold u = x / s rounded
+ *   to nearest even, with s = max|x| * (1 / 127) in fp32, at least 2^-80; they are read as u * s.
+ *   A block is quantised once, from the bf16 rows, when its 64 positions have all left the window: the
+ *   region holds positions [0, D_n), D_n = floor(max(0, T_n - W) / 64) * 64, and the ring keeps the
+ *   deepest plane of the others in bf16.  So the contents do not depend on how the positions were split
+ *   into draft blocks, and the plane rule of ripe_verify_attn is unchanged.
+ *   A block with an infinity, a NaN or a magnitude above 127 * 2^80 reads as NaN in full.
+ * Device layout: records of 128 d + 32 bytes, (max_T - W) / 64 (rounded down) per (layer, sequence, kv
+ * head); ring as for ripe_cache_alloc with S = min(W + max_B + 63, max_T) slots.  stats.deep_rows is the
+ * capacity of the 8-bit region in positions.
+ * On such a cache ripe_append_verify and the draft calls take two launches, and ripe_verify_attn needs
+ * 16-byte aligned q and out (RIPE_EINVAL).
+ */
+int ripe_cache_alloc_q8(int batch, int layers, int q_heads, int kv_heads, int head_dim, int loops, int window,
+                        int max_T, int max_B, int window_mode, ripe_cache_t **out);
+
+/* Bits of a deepest-plane element: 16 or 8 (RIPE_EINVAL for NULL). */
+int ripe_cache_kv_bits(const ripe_cache_t *c);
+
 /* Free a cache and its device memory (synchronises the device first).  NULL is a no-op. */
 int ripe_cache_free(ripe_cache_t *c);
 
@@ -142,6 +165,57 @@ int ripe_load_prefix(ripe_cache_t *c, int layer, int plane, const int32_t *T, co
  */
 int ripe_append_block(ripe_cache_t *c, int layer, int r, int B, const void *k, const void *v,
                       void *stream);
+
+/*
+ * Position rotation (rotary embedding) of keys and queries: the pair (a, b) number i of the first
+ * rotary_dim elements of a head at position p becomes (a cos - b sin, b cos + a sin) with cos[p][i] and
+ * sin[p][i], computed in fp32 and rounded once to bf16; the elements behind stay as they are.
+ *   cos, sin     device fp32 [positions][rotary_dim / 2], 16-byte aligned: any frequency scaling is the
+ *                caller's, in whatever precision far positions need
+ *   rotary_dim   8 .. head_dim, a multiple of 8
+ *   interleaved  0: pair i is elements i and rotary_dim / 2 + i; 1: elements 2 i and 2 i + 1
+ */
+typedef struct ripe_rope {
+    const float *cos, *sin;
+    int32_t positions, rotary_dim, interleaved;
+} ripe_rope;
+
+/*
+ * ripe_append_block with the position rotation applied on the way: the keys of block position j are
+ * rotated by position T_n + j as they are written to the ring, and the queries, when given, into q_out,
+ * in one launch.  The position is read on the device, so that the call needs no host copy of T_n
+ * (ripe_commit_device) and a captured graph follows the lengths.
+ *   k, v     device bf16, token (n, j) at element (n * B + j) * ld_kv, its [kv_heads][d] packed
+ *   q        likewise with ld_q and [q_heads][d], or NULL; q_out packed [batch][B][q_heads][d]
+ *   ld_kv, ld_q  multiples of 8, at least kv_heads * d and q_heads * d: parts of one projection's output
+ *            can be passed in place
+ * Pointers are 16-byte aligned; q_out is q itself (packed) or overlaps no input (else RIPE_EINVAL).
+ * State rules and errors as for ripe_append_block; RIPE_ECAPACITY also if T_n + B > rope->positions.
+ */
+int ripe_append_block_rope(ripe_cache_t *c, int layer, int r, int B, const void *k, const void *v, int64_t ld_kv,
+                           const void *q, int64_t ld_q, void *q_out, const ripe_rope *rope, void *stream);
+
+/*
+ * The same rotation without the append, for the draft calls and ripe_append_verify, which write the keys
+ * themselves: rows of block positions j .. j + B - 1 (j + B <= max_B) are rotated by T_n + j onward.
+ *   k, ld_k, k_out   as q, ld_q, q_out of ripe_append_block_rope with kv_heads; k or q may be NULL
+ * Needs no block or draft in flight and changes no state.
+ */
+int ripe_rotate_block(ripe_cache_t *c, int j, int B, const void *k, int64_t ld_k, void *k_out, const void *q,
+                      int64_t ld_q, void *q_out, const ripe_rope *rope, void *stream);
+
+/*
+ * How scores are formed by every later attention call on this cache (verify, wave, draft, windowed
+ * draft, append_verify), for models trained with it.  With x = scale * <q, K_plane[t]>:
+ *   softcap > 0    x <- softcap * tanh(x / softcap)
+ *   slopes         host fp32[q_heads] or NULL: x <- x - slopes[h] * (p - t), a bias linear in the
+ *                  distance (finite; copied before the call returns; synchronises the stream)
+ * softcap 0 and slopes NULL (the state after allocation) give plain scores again.  Not while the
+ * stream is captured (RIPE_ESTATE); a captured graph keeps the softcap and the presence of slopes that it
+ * was captured with, and reads the slopes of the last call.  With either, the draft calls and
+ * ripe_append_verify take two launches and q and out are 16-byte aligned (RIPE_EINVAL).
+ */
+int ripe_set_scores(ripe_cache_t *c, float softcap, const float *slopes, void *stream);
 
 /*
  * Verification attention of the draft block at loop r for one layer.
@@ -257,6 +331,16 @@ int ripe_cache_stats(const ripe_cache_t *c, ripe_stats *st);
 int ripe_cache_export(ripe_cache_t *c, int n, int layer, void *k_out, void *v_out,
                       uint8_t *plane_present, void *stream);
 
+/*
+ * The 8-bit blocks of one sequence of one layer (ripe_cache_alloc_q8), D_n = floor(max(0, T_n - W) / 64) * 64:
+ *   k_out, v_out      device int8 [kv_heads][D_n][d]
+ *   k_scale, v_scale  device fp32 [kv_heads][D_n / 64]
+ * RIPE_EINVAL for a bf16 cache; requires synced lengths.  (ripe_cache_export of such a cache gives u * s
+ * rounded to bf16 for these positions.)
+ */
+int ripe_cache_export_q8(ripe_cache_t *c, int n, int layer, int8_t *k_out, int8_t *v_out, float *k_scale,
+                         float *v_scale, void *stream);
+
 /* Read and clear the device error word (synchronises `stream`); *err_out gets its bits. */
 int ripe_get_device_error(ripe_cache_t *c, uint32_t *err_out, void *stream);
 
@@ -303,6 +387,18 @@ typedef struct ripe_cache_view {
 
 int ripe_verify_attn_static(const ripe_cache_view *view, int layer, int r, const void *q, void *out,
                             float *lse, float scale, uint32_t *device_error, void *stream);
+
+/*
+ * ripe_append_block_rope over caller-owned buffers: the block rows (block_len positions from
+ * lengths[n] on) of loop r are rotated and written to the view's ring, which ripe_verify_attn_static then
+ * reads.  Without rope (NULL) the rows are only copied.  Allocates nothing, needs no set-up call, and may
+ * be captured.  Arguments as for ripe_append_block_rope; k_deep and v_deep are not used, the ring
+ * is 16-byte aligned.  device_error (not NULL) receives RIPE_DEVERR_CAPACITY when a sequence's block does
+ * not fit max_T or the table (or its length is negative): its rows are then left unwritten.
+ */
+int ripe_append_rope_static(const ripe_cache_view *view, int layer, int r, const void *k, const void *v,
+                            int64_t ld_kv, const void *q, int64_t ld_q, void *q_out, const ripe_rope *rope,
+                            uint32_t *device_error, void *stream);
 
 /* How the library was built: RIPE_BUILD_* bits (no device work, no arguments). */
 int ripe_build_info(void);

@@ -13,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -52,12 +54,17 @@ def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False)
         return lib
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, *FLAGS, f"-I{INCLUDE}", "-shared", "-o", tmp, *sources()]
-    if debug:
-        cmd.insert(1, "-DRIPE_DEBUG")
-    if verbose_ptxas:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
+    extra = (["-DRIPE_DEBUG"] if debug else []) + (["-Xptxas=-v"] if verbose_ptxas else [])
+    with tempfile.TemporaryDirectory(dir=LIBDIR) as objs:
+        def compile_one(src):
+            obj = os.path.join(objs, os.path.basename(src) + ".o")
+            subprocess.check_call([nvcc(), *extra, *ARCH, *FLAGS, f"-I{INCLUDE}", "-c", "-o", obj, src])
+            return obj
+
+        # one nvcc per source: the instances of the attention kernels take minutes in a row
+        with ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+            made = list(pool.map(compile_one, sources()))
+        subprocess.check_call([nvcc(), *ARCH, "-shared", "-o", tmp, *made])
     os.replace(tmp, lib)
     return lib
 

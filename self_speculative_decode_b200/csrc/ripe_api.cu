@@ -1,11 +1,12 @@
 // Host side of the C ABI declared in include/ripe.h: argument and state validation,
 // allocation of the cache regions, TMA descriptors, and the host copy of the state.
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <new>
 
-#include "ripe_common.cuh"
+#include "ripe_score.cuh"
 
 using namespace ripe;
 
@@ -51,6 +52,8 @@ void release(ripe_cache *c) {
     cudaFree(c->part_o);
     cudaFree(c->part_ml);
     cudaFree(c->counters);
+    cudaFree(c->rec8);
+    cudaFree(c->slopes_dev);
     delete c;
 }
 
@@ -93,6 +96,23 @@ bool all_appended(const ripe_cache *c) {
     return true;
 }
 
+int64_t block_rows(const ripe_cache *c, int B) { return static_cast<int64_t>(c->N) * B; }
+
+// the kernels of launch_score read queries in 8-byte and write outputs in 4-byte words
+bool aligned_io(const void *q, const void *out) {
+    return ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+}
+
+// T_n + j + B positions of every sequence have to fit the cache and the rotation's table
+int check_room(const ripe_cache *c, int j, int B, const ripe_rope *rope) {
+    for (int n = 0; n < c->N; ++n)
+        if (c->T[n] + j + B > c->max_T || (rope && c->T[n] + j + B > rope->positions)) return RIPE_ECAPACITY;
+    return RIPE_OK;
+}
+
+int alloc_cache(int batch, int layers, int q_heads, int kv_heads, int head_dim, int loops, int window, int max_T,
+                int max_B, int window_mode, int kv_bits, ripe_cache_t **out);
+
 }  // namespace
 
 extern "C" {
@@ -113,6 +133,21 @@ const char *ripe_strerror(int status) {
 int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_dim, int loops, int window,
                      int max_T, int max_B, int window_mode, ripe_cache_t **out) {
     const NvtxRange nvtx_range("ripe_cache_alloc");
+    return alloc_cache(batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T, max_B, window_mode, 16, out);
+}
+
+int ripe_cache_alloc_q8(int batch, int layers, int q_heads, int kv_heads, int head_dim, int loops, int window,
+                        int max_T, int max_B, int window_mode, ripe_cache_t **out) {
+    const NvtxRange nvtx_range("ripe_cache_alloc_q8");
+    return alloc_cache(batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T, max_B, window_mode, 8, out);
+}
+
+}  // extern "C"
+
+namespace {
+
+int alloc_cache(int batch, int layers, int q_heads, int kv_heads, int head_dim, int loops, int window, int max_T,
+                int max_B, int window_mode, int kv_bits, ripe_cache_t **out) {
     if (!out) return RIPE_EINVAL;
     *out = nullptr;
     if (batch < 1 || batch > kMaxBatch || layers < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads ||
@@ -127,9 +162,17 @@ int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_
     c->N = batch; c->L = layers; c->Hq = q_heads; c->kvH = kv_heads; c->g = q_heads / kv_heads;
     c->d = head_dim; c->R = loops; c->max_T = max_T; c->max_B = max_B; c->mode = window_mode;
     c->W = window > max_T ? max_T : window;  // a window of max_T already keeps every plane
-    const long long s_slots = static_cast<long long>(c->W) + max_B;
+    // an 8-bit region takes whole blocks: up to kQ8Block - 1 positions more wait in the ring
+    const bool q8 = kv_bits == 8;
+    const long long s_slots = static_cast<long long>(c->W) + max_B + (q8 ? kQ8Block - 1 : 0);
     c->ring_slots = static_cast<int>(s_slots < max_T ? s_slots : max_T);
-    c->deep_rows = max_T - c->W;
+    c->kv_bits = kv_bits;
+    c->rec_blocks = q8 ? (max_T - c->W) / kQ8Block : 0;
+    c->rec8 = nullptr;
+    c->softcap = 0.f;
+    c->has_bias = false;
+    c->slopes_dev = nullptr;
+    c->deep_rows = q8 ? c->rec_blocks * kQ8Block : max_T - c->W;
     c->deep_box = (c->deep_rows == 0 || c->deep_rows >= kTileRows) ? kTileRows : c->deep_rows;
     c->ring_box = c->ring_slots < kTileRows ? c->ring_slots : kTileRows;
     c->T.assign(batch, 0);
@@ -149,7 +192,8 @@ int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_
         return RIPE_ECUDA;
     }
     const size_t d = head_dim;
-    const size_t deep_elems = static_cast<size_t>(layers) * batch * kv_heads * c->deep_rows * d;
+    const size_t deep_elems = q8 ? 0 : static_cast<size_t>(layers) * batch * kv_heads * c->deep_rows * d;
+    const size_t rec_bytes = static_cast<size_t>(layers) * batch * kv_heads * c->rec_blocks * q8_record_bytes(head_dim);
     const size_t ring_elems = static_cast<size_t>(layers) * batch * loops * kv_heads * c->ring_slots * d;
     c->part_rows = 16 * cdiv(max_B * c->g, 16);
     if (c->part_rows > 16 && c->part_rows < 32) c->part_rows = 32;
@@ -160,6 +204,7 @@ int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_
               dalloc(&c->Vd, deep_elems * 2, &c->kv_bytes, kv_fill) &&
               dalloc(&c->Kw, ring_elems * 2, &c->kv_bytes, kv_fill) &&
               dalloc(&c->Vw, ring_elems * 2, &c->kv_bytes, kv_fill) &&
+              dalloc(&c->rec8, rec_bytes, &c->kv_bytes, kDebug ? 0xFF : 0) &&
               dalloc(&c->T_dev, batch * sizeof(int32_t), &c->scratch_bytes) &&
               dalloc(&c->err_dev, sizeof(uint32_t), &c->scratch_bytes) &&
               dalloc(&c->part_o, static_cast<size_t>(c->part_slots) * c->part_rows * d * sizeof(float),
@@ -175,13 +220,14 @@ int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_
     std::memset(&c->tm_Vd, 0, sizeof(CUtensorMap));
     const long long deep_pages = static_cast<long long>(layers) * batch * kv_heads;
     const long long ring_pages = static_cast<long long>(layers) * batch * loops * kv_heads;
-    if (c->deep_rows > 0) {
+    if (c->deep_rows > 0 && !q8) {
         ok = encode_map(&c->tm_Kd, c->Kd, head_dim, c->deep_rows, deep_pages, c->deep_box) &&
              encode_map(&c->tm_Vd, c->Vd, head_dim, c->deep_rows, deep_pages, c->deep_box);
     }
     ok = ok && encode_map(&c->tm_Kw, c->Kw, head_dim, c->ring_slots, ring_pages, c->ring_box) &&
          encode_map(&c->tm_Vw, c->Vw, head_dim, c->ring_slots, ring_pages, c->ring_box);
-    if (!ok || ensure_verify_attributes(c->device) != RIPE_OK || cudaDeviceSynchronize() != cudaSuccess) {
+    if (!ok || ensure_verify_attributes(c->device) != RIPE_OK ||
+        (q8 && ensure_score_attributes(c->device) != RIPE_OK) || cudaDeviceSynchronize() != cudaSuccess) {
         cudaGetLastError();
         release(c);
         return RIPE_ECUDA;
@@ -189,6 +235,43 @@ int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_
     *out = c;
     return RIPE_OK;
 }
+
+}  // namespace
+
+extern "C" {
+
+int ripe_set_scores(ripe_cache_t *c, float softcap, const float *slopes, void *stream) {
+    const NvtxRange nvtx_range("ripe_set_scores");
+    if (!c || !(softcap >= 0.f) || std::isinf(softcap)) return RIPE_EINVAL;
+    if (slopes)
+        for (int h = 0; h < c->Hq; ++h)
+            if (!std::isfinite(slopes[h])) return RIPE_EINVAL;
+    DeviceGuard g(c->device);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (!g.ok || cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+        cudaGetLastError();
+        return RIPE_ECUDA;
+    }
+    if (capture != cudaStreamCaptureStatusNone) return RIPE_ESTATE;
+    if (ensure_score_attributes(c->device) != RIPE_OK) return RIPE_ECUDA;
+    if (slopes) {
+        if (!c->slopes_dev && !dalloc(&c->slopes_dev, c->Hq * sizeof(float), &c->scratch_bytes)) return RIPE_ENOMEM;
+        // attention launches on the stream may still read the old slopes; the caller's array is read by the
+        // time the call returns, pinned or not
+        if (cudaMemcpyAsync(c->slopes_dev, slopes, c->Hq * sizeof(float), cudaMemcpyHostToDevice, s) != cudaSuccess ||
+            cudaStreamSynchronize(s) != cudaSuccess) {
+            cudaGetLastError();
+            return RIPE_ECUDA;
+        }
+    }
+    c->softcap = softcap;
+    c->has_bias = slopes != nullptr;
+    c->lengths_dirty = true;  // the next attention launch waits for the copy
+    return RIPE_OK;
+}
+
+int ripe_cache_kv_bits(const ripe_cache_t *c) { return c ? c->kv_bits : RIPE_EINVAL; }
 
 int ripe_cache_free(ripe_cache_t *c) {
     const NvtxRange nvtx_range("ripe_cache_free");
@@ -240,13 +323,51 @@ int ripe_append_block(ripe_cache_t *c, int layer, int r, int B, const void *k, c
     return RIPE_OK;
 }
 
+int ripe_append_block_rope(ripe_cache_t *c, int layer, int r, int B, const void *k, const void *v, int64_t ld_kv,
+                           const void *q, int64_t ld_q, void *q_out, const ripe_rope *rope, void *stream) {
+    const NvtxRange nvtx_range("ripe_append_block_rope");
+    if (!c || !k || !v || !rope || layer < 0 || layer >= c->L || r < 0 || r >= c->R || B < 1 || B > c->max_B)
+        return RIPE_EINVAL;
+    if (c->B_cur != 0 && B != c->B_cur) return RIPE_EINVAL;
+    int st = check_rope(rope, c->d, c->Hq, c->kvH, block_rows(c, B), k, v, ld_kv, q, ld_q, nullptr, q_out);
+    if (st == RIPE_OK) st = check_room(c, 0, B, rope);
+    if (st != RIPE_OK) return st;
+    DeviceGuard g(c->device);
+    if (!g.ok) return RIPE_ECUDA;
+    st = launch_append_rope(c, layer, r, 0, B, k, v, ld_kv, q, ld_q, q_out, rope, static_cast<cudaStream_t>(stream));
+    if (st != RIPE_OK) return st;
+    c->B_cur = B;
+    c->appended[static_cast<size_t>(layer) * c->R + r] = 1;
+    c->prefix_set = true;
+    return RIPE_OK;
+}
+
+int ripe_rotate_block(ripe_cache_t *c, int j, int B, const void *k, int64_t ld_k, void *k_out, const void *q,
+                      int64_t ld_q, void *q_out, const ripe_rope *rope, void *stream) {
+    const NvtxRange nvtx_range("ripe_rotate_block");
+    if (!c || !rope || (!k && !q) || (k == nullptr) != (k_out == nullptr) || j < 0 || B < 1 || j >= c->max_B ||
+        B > c->max_B - j)
+        return RIPE_EINVAL;
+    int st = check_rope(rope, c->d, c->Hq, c->kvH, block_rows(c, B), k, nullptr, ld_k, q, ld_q, k_out, q_out);
+    if (st == RIPE_OK) st = check_room(c, j, B, rope);
+    if (st != RIPE_OK) return st;
+    DeviceGuard g(c->device);
+    if (!g.ok) return RIPE_ECUDA;
+    return launch_rotate(c, j, B, k, ld_k, k_out, q, ld_q, q_out, rope, static_cast<cudaStream_t>(stream));
+}
+
 int ripe_verify_attn(ripe_cache_t *c, int layer, int r, const void *q, void *out, float *lse, float scale,
                      void *stream) {
     const NvtxRange nvtx_range("ripe_verify_attn");
     if (!c || !q || !out || layer < 0 || layer >= c->L || r < 0 || r >= c->R) return RIPE_EINVAL;
     if (c->B_cur == 0 || !c->appended[static_cast<size_t>(layer) * c->R + r]) return RIPE_ESTATE;
+    if (!c->plain() && !aligned_io(q, out)) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
+    if (!c->plain()) {
+        const ScoreCall call = {layer, r, c->B_cur, 0, c->B_cur, 0, -1, nullptr, q, out, lse, scale};
+        return launch_score(c, call, static_cast<cudaStream_t>(stream));
+    }
     return launch_verify(c, layer, r, q, out, lse, scale, static_cast<cudaStream_t>(stream));
 }
 
@@ -261,6 +382,19 @@ int ripe_append_verify(ripe_cache_t *c, int layer, int r, int B, const void *k, 
         if (c->T[n] + B > c->max_T) return RIPE_ECAPACITY;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
+    if (!c->plain()) {
+        if (!aligned_io(q, out) || !aligned_io(k, v)) return RIPE_EINVAL;
+        const int64_t ld = static_cast<int64_t>(c->kvH) * c->d;
+        int st = launch_append_rope(c, layer, r, 0, B, k, v, ld, nullptr, 0, nullptr, nullptr,
+                                    static_cast<cudaStream_t>(stream));
+        const ScoreCall call = {layer, r, B, 0, B, 0, -1, nullptr, q, out, lse, scale};
+        if (st == RIPE_OK) st = launch_score(c, call, static_cast<cudaStream_t>(stream));
+        if (st != RIPE_OK) return st;
+        c->B_cur = B;
+        c->appended[static_cast<size_t>(layer) * c->R + r] = 1;
+        c->prefix_set = true;
+        return RIPE_OK;
+    }
     const int prev_B = c->B_cur;
     c->B_cur = B;  // the kernel plans the block's tiles with this length
     const int st = launch_verify(c, layer, r, q, out, lse, scale, static_cast<cudaStream_t>(stream), k, v);
@@ -284,8 +418,16 @@ static int draft_step(ripe_cache_t *c, int layer, int r, int j, int sink, int wi
         if (c->T[n] + j + 1 > c->max_T) return RIPE_ECAPACITY;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
-    const int st = launch_draft(c, layer, r, j, k, v, q, out, lse, scale, static_cast<cudaStream_t>(stream), sink,
-                                window);
+    int st;
+    if (c->plain()) {
+        st = launch_draft(c, layer, r, j, k, v, q, out, lse, scale, static_cast<cudaStream_t>(stream), sink, window);
+    } else {
+        if (!aligned_io(q, out) || !aligned_io(k, v)) return RIPE_EINVAL;
+        st = launch_append_rope(c, layer, r, j, 1, k, v, static_cast<int64_t>(c->kvH) * c->d, nullptr, 0, nullptr,
+                                nullptr, static_cast<cudaStream_t>(stream));
+        const ScoreCall call = {layer, r, j + 1, j, 1, sink, window, nullptr, q, out, lse, scale};
+        if (st == RIPE_OK) st = launch_score(c, call, static_cast<cudaStream_t>(stream));
+    }
     if (st != RIPE_OK) return st;
     c->drafted[idx] = j + 1;  // a later position of this plane is stale once j is redrafted
     c->prefix_set = true;
@@ -315,8 +457,13 @@ int ripe_verify_attn_wave(ripe_cache_t *c, int layer, const int32_t *loop_of_pos
         if (r < 0 || r >= c->R) return RIPE_EINVAL;
         if (!c->appended[static_cast<size_t>(layer) * c->R + r]) return RIPE_ESTATE;
     }
+    if (!c->plain() && !aligned_io(q, out)) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
+    if (!c->plain()) {
+        const ScoreCall call = {layer, 0, c->B_cur, 0, c->B_cur, 0, -1, loop_of_position, q, out, lse, scale};
+        return launch_score(c, call, static_cast<cudaStream_t>(stream));
+    }
     return launch_verify_wave(c, layer, loop_of_position, q, out, lse, scale, static_cast<cudaStream_t>(stream));
 }
 
@@ -395,6 +542,18 @@ int ripe_cache_export(ripe_cache_t *c, int n, int layer, void *k_out, void *v_ou
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     return launch_export(c, n, layer, k_out, v_out, plane_present, static_cast<cudaStream_t>(stream));
+}
+
+int ripe_cache_export_q8(ripe_cache_t *c, int n, int layer, int8_t *k_out, int8_t *v_out, float *k_scale,
+                         float *v_scale, void *stream) {
+    const NvtxRange nvtx_range("ripe_cache_export_q8");
+    if (!c || c->kv_bits != 8 || !k_out || !v_out || !k_scale || !v_scale || n < 0 || n >= c->N || layer < 0 ||
+        layer >= c->L)
+        return RIPE_EINVAL;
+    if (!c->synced) return RIPE_ESTATE;
+    DeviceGuard g(c->device);
+    if (!g.ok) return RIPE_ECUDA;
+    return launch_q8_export(c, n, layer, k_out, v_out, k_scale, v_scale, static_cast<cudaStream_t>(stream));
 }
 
 int ripe_get_device_error(ripe_cache_t *c, uint32_t *err_out, void *stream) {

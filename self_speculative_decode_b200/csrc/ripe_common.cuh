@@ -85,6 +85,17 @@ struct ripe_cache {
     bool lengths_dirty;
     int64_t kv_bytes, scratch_bytes;
     int64_t launches;
+    // 8-bit deepest-plane region (kv_bits 8; Kd and Vd are then null): records of 64 positions,
+    // [L][N][kvH][rec_blocks], laid out as ripe_score.cuh says
+    int kv_bits, rec_blocks;
+    uint8_t *rec8;
+    // ripe_set_scores
+    float softcap;      // 0: none
+    bool has_bias;
+    float *slopes_dev;  // [Hq]
+    bool scored() const { return softcap > 0.f || has_bias; }
+    // plain scores over a bf16 cache run the verify kernels, everything else launch_score
+    bool plain() const { return kv_bits == 16 && !scored(); }
 };
 
 namespace ripe {
@@ -468,6 +479,32 @@ int launch_load_prefix(ripe_cache *c, int layer, int plane, const int32_t *T, co
 int launch_export(ripe_cache *c, int n, int layer, void *k_out, void *v_out, uint8_t *present,
                   cudaStream_t s);
 int launch_poison(ripe_cache *c, cudaStream_t s);  // debug builds: refill dead rows after a commit
+// Attention over an 8-bit cache or with capped or biased scores (ripe_score.cu): block positions
+// [0, B) in the tile plan, queries at positions j0 .. j0 + qB - 1, at loop r or at loops[j].
+struct ScoreCall {
+    int layer, r, B, j0, qB, sink, window;
+    const int32_t *loops;  // null: every position at loop r
+    const void *q;
+    void *out;
+    float *lse;
+    float scale;
+};
+int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s);
+int ensure_score_attributes(int device);  // as ensure_verify_attributes, for launch_score's kernels
+// The 8-bit region (ripe_q8.cu)
+int launch_q8_load_prefix(ripe_cache *c, int layer, int plane, const int32_t *T, const void *k, const void *v,
+                          int64_t ld_t, cudaStream_t s);
+int launch_q8_evict(ripe_cache *c, const HostIntArray &acc_host, const int32_t *acc_dev, cudaStream_t s);
+int launch_q8_export(ripe_cache *c, int n, int layer, int8_t *k, int8_t *v, float *ks, float *vs, cudaStream_t s);
+int launch_q8_view(ripe_cache *c, int n, int layer, void *k_out, void *v_out, uint8_t *present, cudaStream_t s);
+int launch_q8_poison(ripe_cache *c, cudaStream_t s);
+// Appending with the position rotation (ripe_rope.cu)
+int check_rope(const ripe_rope *rope, int d, int Hq, int kvH, int64_t rows, const void *k, const void *v,
+               int64_t ld_kv, const void *q, int64_t ld_q, const void *k_out, const void *q_out);
+int launch_append_rope(ripe_cache *c, int layer, int r, int j0, int B, const void *k, const void *v, int64_t ld_kv,
+                       const void *q, int64_t ld_q, void *q_out, const ripe_rope *rope, cudaStream_t s);
+int launch_rotate(ripe_cache *c, int j0, int B, const void *k, int64_t ld_k, void *k_out, const void *q, int64_t ld_q,
+                  void *q_out, const ripe_rope *rope, cudaStream_t s);
 // Raise the verify kernels' dynamic shared-memory limit on `device` (which must be current) to
 // what the largest batch needs; once per device, thread-safe.
 int ensure_verify_attributes(int device);

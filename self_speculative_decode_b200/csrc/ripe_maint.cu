@@ -127,7 +127,10 @@ int launch_commit(ripe_cache *c, const int32_t *acc_host, const int32_t *acc_dev
     HostIntArray ah;
     for (int n = 0; n < c->N; ++n) ah.v[n] = acc_host ? acc_host[n] : 0;
     const int d8 = c->d / 8;
-    if (c->deep_rows > 0) {
+    if (c->kv_bits == 8) {
+        const int st = launch_q8_evict(c, ah, acc_dev, s);
+        if (st != RIPE_OK) return st;
+    } else if (c->deep_rows > 0) {
         const int work = c->B_cur * c->kvH * d8;
         int gy = (work + 255) / 256;
         if (gy < 1) gy = 1;
@@ -187,6 +190,7 @@ __global__ void ripe_poison_kernel(uint4 *__restrict__ Kd, uint4 *__restrict__ V
 }
 
 int launch_poison(ripe_cache *c, cudaStream_t s) {
+    if (c->kv_bits == 8) return launch_q8_poison(c, s);
     const int d8 = c->d / 8;
     const size_t rows = static_cast<size_t>(c->L) * c->N * c->kvH * (static_cast<size_t>(c->R) * c->ring_slots +
                                                                       static_cast<size_t>(c->deep_rows));
@@ -237,6 +241,7 @@ __global__ void ripe_load_prefix_kernel(uint4 *__restrict__ Kd, uint4 *__restric
 
 int launch_load_prefix(ripe_cache *c, int layer, int plane, const int32_t *T, const void *k, const void *v,
                        int64_t ld_t, cudaStream_t s) {
+    if (c->kv_bits == 8) return launch_q8_load_prefix(c, layer, plane, T, k, v, ld_t, s);
     HostIntArray th;
     int Tmax = 0;
     for (int n = 0; n < c->N; ++n) {
@@ -300,6 +305,7 @@ __global__ void ripe_export_kernel(const uint4 *__restrict__ Kd, const uint4 *__
 }
 
 int launch_export(ripe_cache *c, int n, int layer, void *k_out, void *v_out, uint8_t *present, cudaStream_t s) {
+    if (c->kv_bits == 8) return launch_q8_view(c, n, layer, k_out, v_out, present, s);
     PlaneMask app;
     for (int p = 0; p < kMaxLoops; ++p) app.v[p] = (p < c->R) ? c->appended[layer * c->R + p] : 0;
     const int Tv = c->T[n] + c->B_cur;

@@ -1,0 +1,193 @@
+// Internal definitions of the attention over caches with an 8-bit deepest-plane region, or with
+// capped or distance-biased scores (ripe_score.cu, ripe_score_q8.cu), and of that region's layout
+// (ripe_q8.cu): the tile plan and the argument block.
+#pragma once
+
+#include "ripe_verify.cuh"
+
+namespace ripe {
+
+// ---------------------------------------------------------------- 8-bit deepest-plane region
+// 64 tokens of one (layer, sequence, kv head) form a block: K and V as signed 8-bit values with one
+// scale each, x = u * s with s = max|x| * (1 / 127).  A block is stored as one record of
+// q8_record_bytes(d), copied to shared memory by one bulk copy:
+//   K bytes [64 d], V bytes [64 d], {K scale, log2 of the V scale, 1 / V scale, V scale}, 16 bytes pad.
+// Bytes hold u + 128 and lie in the order in which the mma.sync m16n8k16 A fragments want them, so a
+// lane reads the bytes of two fragments with one conflict-free 16-byte load and no transpose:
+//   K  (A = K: rows keys, k = head_dim): per 16 keys and 32 columns, lane (g4, c4) holds for each 16
+//      columns the four columns 4 c4 .. 4 c4 + 3 of key g4, then of key g4 + 8 (the order of the
+//      columns inside a k-step is free as long as Q follows it);
+//   V  (A = V^T: rows head_dim, k = keys): per 16 keys and 32 columns, lane (g4, c4) holds for each 16
+//      columns the keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9 of column g4, then of column g4 + 8.
+constexpr int kQ8Block = 64;
+constexpr float kQ8MinScale = 8.271806125530277e-25f;  // 2^-80: the smallest scale
+constexpr float kQ8MaxScale = 1.2089258196146292e24f;  // 2^80: above it the block reads as NaN
+
+__host__ __device__ constexpr int q8_record_bytes(int d) { return 128 * d + 32; }
+
+// offset of key t (0..63), column e inside the K (or V) half of a record
+__host__ __device__ __forceinline__ int q8_k_offset(int t, int e, int d) {
+    const int kb = t >> 4, r = t & 15, ks = e >> 4;
+    const int lane = (r & 7) * 4 + ((e & 15) >> 2);
+    return kb * 16 * d + ((ks >> 1) * 32 + lane) * 16 + (ks & 1) * 8 + (r >> 3) * 4 + (e & 3);
+}
+__host__ __device__ __forceinline__ int q8_v_offset(int t, int e, int d) {
+    const int kb = t >> 4, kk = t & 15, mt = e >> 4, r = e & 15;
+    const int lane = (r & 7) * 4 + ((kk & 7) >> 1);
+    return kb * 16 * d + ((mt >> 1) * 32 + lane) * 16 + (mt & 1) * 8 + (r >> 3) * 4 + (kk & 1) + 2 * (kk >> 3);
+}
+
+// ---------------------------------------------------------------- tile plan
+// As in ripe_common.cuh, with a deepest-plane region that ends at a multiple of `unit` positions (1,
+// or 64 in the 8-bit region: whole blocks), so that up to unit - 1 positions older than the window
+// are still in the ring:
+//   DEEP  [0, D), D = floor(max(0, T - W) / unit) * unit, in tiles of 64 rows (8-bit: two blocks)
+//   RING  plane r, [lo, T + B) with lo the first key that a query sees at plane r; the only loop
+//         being the deepest, [D, T + B), as every key is then read at plane R-1
+//   DUAL  plane R-1, [D, hi): keys older than the window of some query of the call
+struct ScorePlan {
+    int W, B, R, S, unit;
+    int deep_box, ring_box;
+    int crel;         // cache-relative window
+    int all_deepest;  // a single loop, the deepest one
+    int sink, dwin;   // windowed draft (dwin >= 0), as PlanArgs
+    int j0;           // first query's block position
+    int nloops;
+    uint8_t loop[kMaxQueryRows];
+    uint8_t jloop[kMaxQueryRows];
+};
+
+struct ScoreSeg {  // a range of positions in the ring, cut where the ring wraps
+    int p0, len, slot0, first, n1, n;
+};
+
+struct ScoreGeom {
+    int T, D;
+    int e1, b2, nd1, nd;  // DEEP rows [0, e1) in nd1 tiles, then [b2, D)
+    ScoreSeg ring, dual;
+    int total;
+};
+
+__host__ __device__ __forceinline__ ScoreSeg score_seg(int p0, int len, const ScorePlan &a) {
+    ScoreSeg s;
+    s.p0 = p0;
+    s.len = len > 0 ? len : 0;
+    s.slot0 = p0 % a.S;
+    s.first = s.len < a.S - s.slot0 ? s.len : a.S - s.slot0;
+    s.n1 = ctiles(s.first, a.ring_box);
+    s.n = s.n1 + ctiles(s.len - s.first, a.ring_box);
+    return s;
+}
+
+__host__ __device__ __forceinline__ ScoreGeom score_geom(int T, const ScorePlan &a) {
+    ScoreGeom s;
+    const int A = T - a.W > 0 ? T - a.W : 0;
+    const int tr = a.unit > 1 ? 2 * kQ8Block : kTileRows;
+    s.T = T;
+    s.D = a.unit > 1 ? A & ~(kQ8Block - 1) : A;
+    s.e1 = s.b2 = 0;
+    if (a.dwin >= 0) {
+        const int se = a.sink < s.D ? (a.sink + 63) & ~63 : s.D;
+        s.e1 = se < s.D ? se : s.D;
+        int ws = T + a.j0 - a.dwin;
+        ws = ws < 0 ? 0 : ws > s.D ? s.D : ws;
+        s.b2 = (ws & ~63) > s.e1 ? ws & ~63 : s.e1;
+    }
+    s.nd1 = cdiv(s.e1, tr);
+    s.nd = s.nd1 + cdiv(s.D - s.b2, tr);
+    if (a.all_deepest) {
+        s.ring = score_seg(s.D, T + a.B - s.D, a);
+        s.dual = score_seg(s.D, 0, a);
+    } else {
+        int lo = a.crel ? A : T + a.j0 - a.W;
+        lo = lo < 0 ? 0 : lo > T ? T : lo;
+        int hi = a.crel ? A : T + a.B - 1 - a.W;
+        hi = hi < T ? hi : T;
+        s.ring = score_seg(lo, T + a.B - lo, a);
+        s.dual = score_seg(s.D, hi - s.D, a);
+    }
+    s.total = s.nd + a.nloops * s.ring.n + s.dual.n;
+    return s;
+}
+
+__host__ __device__ __forceinline__ Tile score_tile(const ScoreGeom &s, int lt, const ScorePlan &a) {
+    Tile t;
+    if (lt < s.nd) {
+        const int tr = a.unit > 1 ? 2 * kQ8Block : kTileRows;
+        const bool head = lt < s.nd1;
+        t.kind = kDeep;
+        t.plane = a.R - 1;
+        t.t0 = head ? lt * tr : s.b2 + (lt - s.nd1) * tr;
+        const int end = head ? s.e1 : s.D;
+        t.cnt = end - t.t0 < tr ? end - t.t0 : tr;
+        t.y = t.t0;
+        return t;
+    }
+    lt -= s.nd;
+    const ScoreSeg *g = &s.dual;
+    t.kind = kDual;
+    t.plane = a.R - 1;
+    if (lt < a.nloops * s.ring.n) {
+        int k = 0;
+        while (lt >= s.ring.n) { lt -= s.ring.n; ++k; }
+        g = &s.ring;
+        t.kind = kRing;
+        t.plane = a.loop[k];
+    } else {
+        lt -= a.nloops * s.ring.n;
+    }
+    int off, end;
+    if (lt < g->n1) {
+        off = lt * a.ring_box;
+        end = g->first;
+        t.y = g->slot0 + off;
+    } else {
+        off = g->first + (lt - g->n1) * a.ring_box;
+        end = g->len;
+        t.y = off - g->first;
+    }
+    t.t0 = g->p0 + off;
+    t.cnt = end - off < a.ring_box ? end - off : a.ring_box;
+    return t;
+}
+
+// Whether the query of block position jq (loop lq) sees key t of a tile of this kind and plane.
+__host__ __device__ __forceinline__ bool score_sees(const ScorePlan &a, int T, int kind, int plane, int t, int jq,
+                                                    int lq) {
+    const int p = T + jq;
+    bool vis = true;
+    if (kind == kRing)
+        vis = lq == plane && t <= p && (a.all_deepest || a.crel || t >= T || t >= p - a.W);
+    else if (kind == kDual)
+        vis = a.crel || t < p - a.W;
+    if (a.dwin >= 0) vis = vis && (t < a.sink || t >= p - a.dwin);
+    return vis;
+}
+
+// ---------------------------------------------------------------- arguments of one launch
+struct ScoreArgs {
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *out;
+    float *lse;
+    const int32_t *T;
+    float *part_o, *part_ml;
+    int32_t *counters;
+    uint32_t *err;
+    const uint8_t *rec;   // 8-bit records [L][N][kvH][rec_blocks]
+    int rec_blocks;
+    const float *slopes;  // [Hq] distance bias per key; nullptr: none
+    ScorePlan plan;
+    int N, kvH, g, Hq, layer, Mq, min_chunk, qB;
+    int has_deep, early;  // as VerifyArgs
+    float sx;             // factor of the dot product: scale * log2(e), or 2 scale log2(e) / cap
+    float cap;            // cap * log2(e), 0: no cap
+    int dbg_deep_rows, dbg_part_slots;
+    long long dbg_ring_pages;
+};
+
+cudaError_t launch_score_q8(int d, bool mod, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
+cudaError_t launch_score_bf16(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
+cudaError_t set_score_q8_attributes();
+cudaError_t set_score_bf16_attributes();
+
+}  // namespace ripe

@@ -28,7 +28,8 @@ EXPORTS = (
     "ripe_cache_stats", "ripe_cache_export", "ripe_get_device_error", "ripe_launch_count",
     "ripe_strerror", "ripe_verify_attn_static", "ripe_verify_attn_wave", "ripe_append_verify",
     "ripe_draft_attn", "ripe_draft_attn_window", "ripe_build_info", "ripe_set_verify_consumer",
-    "ripe_get_verify_consumer",
+    "ripe_get_verify_consumer", "ripe_cache_alloc_q8", "ripe_cache_kv_bits", "ripe_cache_export_q8",
+    "ripe_set_scores", "ripe_append_block_rope", "ripe_rotate_block", "ripe_append_rope_static",
 )
 RIPE_ESCRATCH = -6
 RIPE_STATIC_SCRATCH_BYTES = 4 << 20
@@ -53,6 +54,12 @@ class CacheView(ctypes.Structure):
                 ("batch", "layers", "q_heads", "kv_heads", "head_dim", "loops", "window", "max_T",
                  "max_B", "window_mode", "block_len")] + \
                [(name, ctypes.c_void_p) for name in ("k_deep", "v_deep", "k_ring", "v_ring", "lengths")]
+
+
+class Rope(ctypes.Structure):
+    """ripe_rope: cos and sin tables of the position rotation (RotaryTable holds the tensors)."""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p)] + \
+               [(name, ctypes.c_int32) for name in ("positions", "rotary_dim", "interleaved")]
 
 
 _lib = None
@@ -90,6 +97,14 @@ def lib() -> ctypes.CDLL:
             "ripe_append_verify": ([vp, i, i, i, vp, vp, vp, vp, vp, ctypes.c_float, vp], i),
             "ripe_draft_attn": ([vp, i, i, i, vp, vp, vp, vp, vp, ctypes.c_float, vp], i),
             "ripe_draft_attn_window": ([vp, i, i, i, i, i, vp, vp, vp, vp, vp, ctypes.c_float, vp], i),
+            "ripe_cache_alloc_q8": ([i] * 10 + [ctypes.POINTER(vp)], i),
+            "ripe_cache_kv_bits": ([vp], i),
+            "ripe_cache_export_q8": ([vp, i, i, vp, vp, vp, vp, vp], i),
+            "ripe_set_scores": ([vp, ctypes.c_float, ctypes.POINTER(ctypes.c_float), vp], i),
+            "ripe_append_block_rope": ([vp, i, i, i, vp, vp, i64, vp, i64, vp, ctypes.POINTER(Rope), vp], i),
+            "ripe_rotate_block": ([vp, i, i, vp, i64, vp, vp, i64, vp, ctypes.POINTER(Rope), vp], i),
+            "ripe_append_rope_static": ([ctypes.POINTER(CacheView), i, i, vp, vp, i64, vp, i64, vp,
+                                         ctypes.POINTER(Rope), vp, vp], i),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -127,6 +142,25 @@ def _dev(t, dtype, shape, name):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t, dtype, shape, name):
+    """Pointer and token stride (elements) of a [N][B][heads][d] tensor whose heads are packed and whose tokens
+    lie at one stride, as a part of a projection's output does."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    N, B, H, d = shape
+    s = t.stride()
+    # the stride of a dimension of one element says nothing
+    ld = s[1] if B > 1 else s[0] if N > 1 else H * d
+    if s[3] != 1 or (H > 1 and s[2] != d) or (N > 1 and B > 1 and s[0] != B * ld):
+        raise ValueError(f"{name} must have packed heads and evenly spaced tokens, got strides {tuple(s)}")
+    return t.data_ptr(), ld
 
 
 def _ints(values, n):
@@ -229,6 +263,52 @@ def ripe_verify_attn_static(view, layer, r, q, out, lse=None, scale=1.0, device_
            "ripe_verify_attn_static")
 
 
+def ripe_cache_alloc_q8(batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T, max_B,
+                        window_mode=RIPE_WINDOW_QUERY_RELATIVE):
+    h = ctypes.c_void_p()
+    _check(lib().ripe_cache_alloc_q8(batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T,
+                                     max_B, window_mode, ctypes.byref(h)), "ripe_cache_alloc_q8")
+    return h
+
+
+def ripe_cache_kv_bits(h):
+    bits = lib().ripe_cache_kv_bits(h)
+    _check(bits if bits < 0 else RIPE_OK, "ripe_cache_kv_bits")
+    return bits
+
+
+def ripe_cache_export_q8(h, n, layer, k_out, v_out, k_scale, v_scale, stream=None):
+    _check(lib().ripe_cache_export_q8(h, n, layer, ctypes.c_void_p(k_out), ctypes.c_void_p(v_out),
+                                      ctypes.c_void_p(k_scale), ctypes.c_void_p(v_scale), _stream(stream)),
+           "ripe_cache_export_q8")
+
+
+def ripe_set_scores(h, softcap=0.0, slopes=None, stream=None):
+    """slopes: a sequence of q_heads floats (the caller checks the length), or None."""
+    arr = None if slopes is None else (ctypes.c_float * len(slopes))(*[float(x) for x in slopes])
+    _check(lib().ripe_set_scores(h, float(softcap), arr, _stream(stream)), "ripe_set_scores")
+
+
+def ripe_append_block_rope(h, layer, r, B, k, v, ld_kv, q, ld_q, q_out, rope, stream=None):
+    _check(lib().ripe_append_block_rope(h, layer, r, B, ctypes.c_void_p(k), ctypes.c_void_p(v), ld_kv,
+                                        ctypes.c_void_p(q or 0), ld_q, ctypes.c_void_p(q_out or 0),
+                                        ctypes.byref(rope), _stream(stream)), "ripe_append_block_rope")
+
+
+def ripe_rotate_block(h, j, B, k, ld_k, k_out, q, ld_q, q_out, rope, stream=None):
+    _check(lib().ripe_rotate_block(h, j, B, ctypes.c_void_p(k or 0), ld_k, ctypes.c_void_p(k_out or 0),
+                                   ctypes.c_void_p(q or 0), ld_q, ctypes.c_void_p(q_out or 0), ctypes.byref(rope),
+                                   _stream(stream)), "ripe_rotate_block")
+
+
+def ripe_append_rope_static(view, layer, r, k, v, ld_kv, q, ld_q, q_out, rope, device_error, stream=None):
+    """Append over caller-owned buffers (see include/ripe.h); pointers are ints, rope a Rope or None."""
+    _check(lib().ripe_append_rope_static(ctypes.byref(view), layer, r, ctypes.c_void_p(k), ctypes.c_void_p(v), ld_kv,
+                                         ctypes.c_void_p(q or 0), ld_q, ctypes.c_void_p(q_out or 0),
+                                         None if rope is None else ctypes.byref(rope),
+                                         ctypes.c_void_p(device_error), _stream(stream)), "ripe_append_rope_static")
+
+
 def ripe_launch_count(h):
     return lib().ripe_launch_count(h)
 
@@ -250,8 +330,49 @@ def ripe_get_verify_consumer():
 
 
 # ------------------------------------------------------------------ tensor-level wrapper
+class RotaryTable:
+    """cos and sin of the position rotation: fp32 [positions][rotary_dim / 2], contiguous, on the cache's device.
+
+    ``interleaved``: a pair is elements 2 i and 2 i + 1 of a head; else i and rotary_dim / 2 + i."""
+
+    def __init__(self, cos, sin, interleaved=False):
+        import torch
+        if cos.dim() != 2:
+            raise ValueError("cos must be [positions][rotary_dim / 2]")
+        self.cos, self.sin = cos, sin  # the struct below points into them
+        self.rope = Rope(cos=_dev(cos, torch.float32, None, "cos").value,
+                         sin=_dev(sin, torch.float32, cos.shape, "sin").value, positions=cos.shape[0],
+                         rotary_dim=2 * cos.shape[1], interleaved=1 if interleaved else 0)
+
+
+def append_rope_static(view, layer, r, k, v, q=None, table=None, q_out=None, device_error=None, stream=None):
+    """ripe_append_rope_static with tensors: k, v [N][B][kvH][d] and q [N][B][Hq][d] (tokens may be strided) into the
+    ring of ``view`` (a CacheView) and into ``q_out``, which is returned.  ``table``: a RotaryTable, or None to copy
+    without rotating.  ``device_error``: an int32 tensor of one element that collects RIPE_DEVERR_* bits."""
+    import torch
+    N, B = view.batch, view.block_len
+    kp, ld_kv = _rows(k, torch.bfloat16, (N, B, view.kv_heads, view.head_dim), "k")
+    vp, ld_v = _rows(v, torch.bfloat16, (N, B, view.kv_heads, view.head_dim), "v")
+    if ld_v != ld_kv:
+        raise ValueError("k and v must have the same token stride")
+    if device_error is None:
+        raise ValueError("device_error must be given")
+    qp, ld_q, qo = None, 0, None
+    if q is not None:
+        shape = (N, B, view.q_heads, view.head_dim)
+        qp, ld_q = _rows(q, torch.bfloat16, shape, "q")
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+        qo = _dev(q_out, torch.bfloat16, shape, "q_out").value
+    ripe_append_rope_static(view, layer, r, kp, vp, ld_kv, qp, ld_q, qo, None if table is None else table.rope,
+                            _dev(device_error, torch.int32, (1,), "device_error").value, stream)
+    return q_out
+
+
 class RipeCache:
     """A RIPE cache on the current CUDA device, driven with torch tensors.
+
+    ``kv_bits``: 16, or 8 to hold the deepest-plane region in 8 bits with a scale for each 64 positions.
 
     Shapes (bf16, contiguous, on the cache's device):
       prefix plane  k, v [N][kvH][ld_t][d]
@@ -260,14 +381,17 @@ class RipeCache:
     """
 
     def __init__(self, batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T, max_B,
-                 window_mode=RIPE_WINDOW_QUERY_RELATIVE):
+                 window_mode=RIPE_WINDOW_QUERY_RELATIVE, kv_bits=16):
         import torch
+        if kv_bits not in (8, 16):
+            raise ValueError("kv_bits must be 8 or 16")
         if not torch.cuda.is_available():
             raise RuntimeError("RipeCache needs a CUDA device")
         self.N, self.L, self.Hq, self.kvH, self.d = batch, layers, q_heads, kv_heads, head_dim
         self.R, self.W, self.max_T, self.max_B, self.mode = loops, window, max_T, max_B, window_mode
-        self.handle = ripe_cache_alloc(batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T,
-                                       max_B, window_mode)
+        self.kv_bits = kv_bits
+        self.handle = (ripe_cache_alloc if kv_bits == 16 else ripe_cache_alloc_q8)(
+            batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T, max_B, window_mode)
 
     def close(self):
         if self.handle is not None and self.handle.value:
@@ -293,6 +417,46 @@ class RipeCache:
         shape = (self.N, B, self.kvH, self.d)
         ripe_append_block(self.handle, layer, r, B, _dev(k, torch.bfloat16, shape, "k").value,
                           _dev(v, torch.bfloat16, shape, "v").value, stream)
+
+    def set_scores(self, softcap=0.0, slopes=None, stream=None):
+        """Capped scores (softcap > 0) and a bias -slopes[h] * distance (Hq floats) in every later attention call."""
+        if slopes is not None:
+            slopes = slopes.tolist() if hasattr(slopes, "tolist") else list(slopes)
+            if len(slopes) != self.Hq:
+                raise ValueError(f"expected {self.Hq} slopes")
+        ripe_set_scores(self.handle, softcap, slopes, stream)
+
+    def append_block_rope(self, layer, r, k, v, table, q=None, q_out=None, stream=None):
+        """append_block with k, and q if given, rotated by their positions; k, v and q may be parts of one projection's
+        output (tokens strided).  Returns q_out."""
+        import torch
+        B = k.shape[1]
+        kp, ld_kv = _rows(k, torch.bfloat16, (self.N, B, self.kvH, self.d), "k")
+        vp, ld_v = _rows(v, torch.bfloat16, (self.N, B, self.kvH, self.d), "v")
+        if ld_v != ld_kv:
+            raise ValueError("k and v must have the same token stride")
+        qp, ld_q, q_out, qo = self._rotated(q, q_out, B, self.Hq, "q")
+        ripe_append_block_rope(self.handle, layer, r, B, kp, vp, ld_kv, qp, ld_q, qo, table.rope, stream)
+        return q_out
+
+    def rotate_block(self, j, table, k=None, q=None, k_out=None, q_out=None, stream=None):
+        """k [N][B][kvH][d] and q [N][B][Hq][d] of block positions j .. j + B - 1 rotated, for the draft calls and
+        append_verify; returns (k_out, q_out)."""
+        B = (k if k is not None else q).shape[1]
+        kp, ld_k, k_out, ko = self._rotated(k, k_out, B, self.kvH, "k")
+        qp, ld_q, q_out, qo = self._rotated(q, q_out, B, self.Hq, "q")
+        ripe_rotate_block(self.handle, j, B, kp, ld_k, ko, qp, ld_q, qo, table.rope, stream)
+        return k_out, q_out
+
+    def _rotated(self, x, x_out, B, heads, name):
+        import torch
+        if x is None:
+            return None, 0, None, None
+        shape = (self.N, B, heads, self.d)
+        p, ld = _rows(x, torch.bfloat16, shape, name)
+        if x_out is None:
+            x_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        return p, ld, x_out, _dev(x_out, torch.bfloat16, shape, name + "_out").value
 
     def verify_attn(self, layer, r, q, out=None, lse=None, scale=1.0, stream=None):
         import torch
@@ -384,6 +548,19 @@ class RipeCache:
         if Tv:
             ripe_cache_export(self.handle, n, layer, k.data_ptr(), v.data_ptr(), present.data_ptr(), stream)
         return k, v, present
+
+    def export_q8(self, n, layer, stream=None):
+        """8-bit blocks of sequence n, layer: k, v int8 [kvH][D][d] and their scales fp32 [kvH][D / 64]."""
+        import torch
+        if not self.stats()["lengths_synced"]:
+            raise RipeError(RIPE_ESTATE, "export_q8")
+        blocks = max(0, self.sync_lengths(stream)[n] - self.W) // 64
+        dev = torch.device("cuda", torch.cuda.current_device())
+        k, v = (torch.empty((self.kvH, 64 * blocks, self.d), dtype=torch.int8, device=dev) for _ in range(2))
+        ks, vs = (torch.empty((self.kvH, blocks), dtype=torch.float32, device=dev) for _ in range(2))
+        if blocks or self.kv_bits != 8:
+            ripe_cache_export_q8(self.handle, n, layer, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), stream)
+        return k, v, ks, vs
 
     def device_error(self, stream=None):
         return ripe_get_device_error(self.handle, stream)
