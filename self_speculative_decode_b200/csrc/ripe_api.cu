@@ -96,6 +96,9 @@ bool all_appended(const ripe_cache *c) {
     return true;
 }
 
+// arrival counters: one per (sequence, kv head), or two (launch_score takes more than 32 query rows in two groups)
+size_t counter_bytes(const ripe_cache *c) { return 2 * static_cast<size_t>(c->N) * c->kvH * sizeof(int32_t); }
+
 int64_t block_rows(const ripe_cache *c, int B) { return static_cast<int64_t>(c->N) * B; }
 
 // the kernels of launch_score read queries in 8-byte and write outputs in 4-byte words
@@ -211,7 +214,7 @@ int alloc_cache(int batch, int layers, int q_heads, int kv_heads, int head_dim, 
                      &c->scratch_bytes) &&
               dalloc(&c->part_ml, static_cast<size_t>(c->part_slots) * c->part_rows * 4 * sizeof(float),
                      &c->scratch_bytes) &&
-              dalloc(&c->counters, static_cast<size_t>(batch) * kv_heads * sizeof(int32_t), &c->scratch_bytes);
+              dalloc(&c->counters, counter_bytes(c), &c->scratch_bytes);
     if (!ok) {
         release(c);
         return RIPE_ENOMEM;
@@ -226,6 +229,11 @@ int alloc_cache(int batch, int layers, int q_heads, int kv_heads, int head_dim, 
     }
     ok = ok && encode_map(&c->tm_Kw, c->Kw, head_dim, c->ring_slots, ring_pages, c->ring_box) &&
          encode_map(&c->tm_Vw, c->Vw, head_dim, c->ring_slots, ring_pages, c->ring_box);
+    if (q8) {
+        const int box = c->ring_box < kWideRingRows ? c->ring_box : kWideRingRows;
+        ok = ok && encode_map(&c->tm_Kw32, c->Kw, head_dim, c->ring_slots, ring_pages, box) &&
+             encode_map(&c->tm_Vw32, c->Vw, head_dim, c->ring_slots, ring_pages, box);
+    }
     if (!ok || ensure_verify_attributes(c->device) != RIPE_OK ||
         (q8 && ensure_score_attributes(c->device) != RIPE_OK) || cudaDeviceSynchronize() != cudaSuccess) {
         cudaGetLastError();
@@ -569,8 +577,7 @@ int ripe_get_device_error(ripe_cache_t *c, uint32_t *err_out, void *stream) {
     *err_out = e;
     if (e) {  // a kernel stopped early: clear the word and the merge counters it may have left
         if (cudaMemsetAsync(c->err_dev, 0, sizeof(uint32_t), s) != cudaSuccess ||
-            cudaMemsetAsync(c->counters, 0, static_cast<size_t>(c->N) * c->kvH * sizeof(int32_t), s) !=
-                cudaSuccess ||
+            cudaMemsetAsync(c->counters, 0, counter_bytes(c), s) != cudaSuccess ||
             cudaStreamSynchronize(s) != cudaSuccess)
             return RIPE_ECUDA;
     }

@@ -88,6 +88,7 @@ struct ripe_cache {
     // 8-bit deepest-plane region (kv_bits 8; Kd and Vd are then null): records of 64 positions,
     // [L][N][kvH][rec_blocks], laid out as ripe_score.cuh says
     int kv_bits, rec_blocks;
+    CUtensorMap tm_Kw32, tm_Vw32;  // the ring in boxes of at most 32 rows
     uint8_t *rec8;
     // ripe_set_scores
     float softcap;      // 0: none

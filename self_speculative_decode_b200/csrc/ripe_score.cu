@@ -27,6 +27,7 @@ int ensure_score_attributes(int device) {
     std::lock_guard<std::mutex> lock(mu);
     if (done[device]) return RIPE_OK;
     cudaError_t e = set_score_q8_attributes();  // the caller makes the device current
+    if (e == cudaSuccess) e = set_score_q8_mod_attributes();
     if (e == cudaSuccess) e = set_score_bf16_attributes();
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -56,8 +57,13 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     p.R = c->R;
     p.S = c->ring_slots;
     p.unit = q8 ? kQ8Block : 1;
+    a.Mq = call.qB * c->g;
+    a.groups = cdiv(a.Mq, kGroupRows);
+    a.grows = cdiv(a.Mq, a.groups);
+    const bool wide = q8 && a.grows > 16;
     p.deep_box = c->deep_box;
-    p.ring_box = c->ring_box;
+    p.deep_tile = q8 && !wide ? 2 * kQ8Block : kTileRows;
+    p.ring_box = wide && c->ring_box > kWideRingRows ? kWideRingRows : c->ring_box;
     p.crel = c->mode == RIPE_WINDOW_CACHE_RELATIVE ? 1 : 0;
     p.sink = call.sink;
     p.dwin = call.window;
@@ -77,7 +83,6 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     a.Hq = c->Hq;
     a.layer = call.layer;
     a.qB = call.qB;
-    a.Mq = call.qB * c->g;
     a.min_chunk = RIPE_MIN_CHUNK;
     a.has_deep = !q8 && c->deep_rows > 0 ? 1 : 0;
     a.early = c->lengths_dirty ? 0 : 1;
@@ -85,19 +90,22 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     a.cap = c->softcap * log2e;
     a.sx = c->softcap > 0.f ? 2.f * call.scale * log2e / c->softcap : call.scale * log2e;
     a.dbg_deep_rows = c->deep_rows;
-    a.dbg_part_slots = c->part_slots;
+    // partials of two groups of 32 rows take the room of one of 64 (ripe_cache_alloc's scratch)
+    a.dbg_part_slots = c->num_sms + c->N * c->kvH * a.groups;
 
     // grid: one CTA per SM, fewer when the host copy of T says there is less work
     int grid = c->num_sms < 256 ? c->num_sms : 256;
     if (c->synced) {
         long total = 0;
-        for (int n = 0; n < c->N; ++n) total += static_cast<long>(score_geom(c->T[n], p).total) * c->kvH;
+        for (int n = 0; n < c->N; ++n) total += static_cast<long>(score_geom(c->T[n], p).total) * c->kvH * a.groups;
         const long need = (total + a.min_chunk - 1) / a.min_chunk;
         if (need < grid) grid = static_cast<int>(need);
     }
     if (grid < 1) grid = 1;
-    const LaunchTarget t = {&c->tm_Kd, &c->tm_Vd, &c->tm_Kw, &c->tm_Vw, c->device, c->num_sms, c->N};
-    const cudaError_t e = q8 ? launch_score_q8(c->d, c->scored(), t, grid, a, s) : launch_score_bf16(c->d, t, grid, a, s);
+    const LaunchTarget t = {&c->tm_Kd, &c->tm_Vd, wide ? &c->tm_Kw32 : &c->tm_Kw, wide ? &c->tm_Vw32 : &c->tm_Vw,
+                            c->device, c->num_sms, c->N};
+    const auto launch = !q8 ? launch_score_bf16 : c->scored() ? launch_score_q8_mod : launch_score_q8;
+    const cudaError_t e = launch(c->d, t, grid, a, s);
     c->launches += 1;
     c->lengths_dirty = false;
     return e == cudaSuccess ? RIPE_OK : RIPE_ECUDA;

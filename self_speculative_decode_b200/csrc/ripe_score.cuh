@@ -41,13 +41,14 @@ __host__ __device__ __forceinline__ int q8_v_offset(int t, int e, int d) {
 // As in ripe_common.cuh, with a deepest-plane region that ends at a multiple of `unit` positions (1,
 // or 64 in the 8-bit region: whole blocks), so that up to unit - 1 positions older than the window
 // are still in the ring:
-//   DEEP  [0, D), D = floor(max(0, T - W) / unit) * unit, in tiles of 64 rows (8-bit: two blocks)
+//   DEEP  [0, D), D = floor(max(0, T - W) / unit) * unit, in tiles of deep_tile rows
 //   RING  plane r, [lo, T + B) with lo the first key that a query sees at plane r; the only loop
 //         being the deepest, [D, T + B), as every key is then read at plane R-1
 //   DUAL  plane R-1, [D, hi): keys older than the window of some query of the call
 struct ScorePlan {
     int W, B, R, S, unit;
     int deep_box, ring_box;
+    int deep_tile;    // rows of a DEEP tile: 64, or 128 (two 8-bit blocks)
     int crel;         // cache-relative window
     int all_deepest;  // a single loop, the deepest one
     int sink, dwin;   // windowed draft (dwin >= 0), as PlanArgs
@@ -82,7 +83,7 @@ __host__ __device__ __forceinline__ ScoreSeg score_seg(int p0, int len, const Sc
 __host__ __device__ __forceinline__ ScoreGeom score_geom(int T, const ScorePlan &a) {
     ScoreGeom s;
     const int A = T - a.W > 0 ? T - a.W : 0;
-    const int tr = a.unit > 1 ? 2 * kQ8Block : kTileRows;
+    const int tr = a.deep_tile;
     s.T = T;
     s.D = a.unit > 1 ? A & ~(kQ8Block - 1) : A;
     s.e1 = s.b2 = 0;
@@ -113,7 +114,7 @@ __host__ __device__ __forceinline__ ScoreGeom score_geom(int T, const ScorePlan 
 __host__ __device__ __forceinline__ Tile score_tile(const ScoreGeom &s, int lt, const ScorePlan &a) {
     Tile t;
     if (lt < s.nd) {
-        const int tr = a.unit > 1 ? 2 * kQ8Block : kTileRows;
+        const int tr = a.deep_tile;
         const bool head = lt < s.nd1;
         t.kind = kDeep;
         t.plane = a.R - 1;
@@ -151,20 +152,32 @@ __host__ __device__ __forceinline__ Tile score_tile(const ScoreGeom &s, int lt, 
     return t;
 }
 
-// Whether the query of block position jq (loop lq) sees key t of a tile of this kind and plane.
+// The keys [lo, hi) of a tile of this kind and plane that the query of block position jq (loop lq) sees, before
+// the tile's own end and a draft window.
+__host__ __device__ __forceinline__ void score_range(const ScorePlan &a, int T, int kind, int plane, int jq, int lq,
+                                                     int &lo, int &hi) {
+    const int p = T + jq;
+    lo = 0;
+    hi = T;  // deepest-plane rows are all older than every query's window
+    if (kind == kRing) {
+        hi = lq == plane ? p + 1 : 0;
+        if (!a.all_deepest && !a.crel) lo = p - a.W < T ? p - a.W : T;
+    } else if (kind == kDual && !a.crel) {
+        hi = p - a.W;
+    }
+}
+
 __host__ __device__ __forceinline__ bool score_sees(const ScorePlan &a, int T, int kind, int plane, int t, int jq,
                                                     int lq) {
-    const int p = T + jq;
-    bool vis = true;
-    if (kind == kRing)
-        vis = lq == plane && t <= p && (a.all_deepest || a.crel || t >= T || t >= p - a.W);
-    else if (kind == kDual)
-        vis = a.crel || t < p - a.W;
-    if (a.dwin >= 0) vis = vis && (t < a.sink || t >= p - a.dwin);
-    return vis;
+    int lo, hi;
+    score_range(a, T, kind, plane, jq, lq, lo, hi);
+    return t >= lo && t < hi && (a.dwin < 0 || t < a.sink || t >= T + jq - a.dwin);
 }
 
 // ---------------------------------------------------------------- arguments of one launch
+constexpr int kGroupRows = 32;
+constexpr int kWideRingRows = 32;  // ring tile of an 8-bit cache with more than 16 rows: as many bytes as a block
+
 struct ScoreArgs {
     const __nv_bfloat16 *q;
     __nv_bfloat16 *out;
@@ -178,6 +191,7 @@ struct ScoreArgs {
     const float *slopes;  // [Hq] distance bias per key; nullptr: none
     ScorePlan plan;
     int N, kvH, g, Hq, layer, Mq, min_chunk, qB;
+    int groups, grows;    // a kv head's Mq query rows in row groups of grows <= kGroupRows
     int has_deep, early;  // as VerifyArgs
     float sx;             // factor of the dot product: scale * log2(e), or 2 scale log2(e) / cap
     float cap;            // cap * log2(e), 0: no cap
@@ -185,9 +199,11 @@ struct ScoreArgs {
     long long dbg_ring_pages;
 };
 
-cudaError_t launch_score_q8(int d, bool mod, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
+cudaError_t launch_score_q8(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
+cudaError_t launch_score_q8_mod(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
 cudaError_t launch_score_bf16(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
 cudaError_t set_score_q8_attributes();
+cudaError_t set_score_q8_mod_attributes();
 cudaError_t set_score_bf16_attributes();
 
 }  // namespace ripe

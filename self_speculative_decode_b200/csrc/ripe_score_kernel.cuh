@@ -16,7 +16,13 @@
 //     f16 values (0x6400 | u + 128 is 1152 + u).  Integers up to 127 are exact in f16 and in bf16; f16
 //     takes two instructions a pair, bf16 four (its 7 mantissa bits cannot hold u + 128).
 //   * Q of those tiles is bf16 scaled by a power of two per row into f16's range, exact for elements
-//     down to 2^-18 of the row's largest; P is rounded to f16 (2^-11 relative).
+//     down to 2^-18 of the row's largest; P is rounded to f16 (2^-11 relative).  Q lies in shared memory in
+//     fragment order, once in each form.
+//   * From 17 rows on (WIDE) the four warps of a tile group split the keys for S and head_dim for O: a warp
+//     turns its 16 keys of K and its quarter of V into f16 for all 32 rows, once, and P goes from one product
+//     to the other through shared memory.  O then takes 32 registers a thread instead of 128, so that three
+//     tile groups fit an SM and hide one another's latencies.  More than 32 rows of a kv head are two groups
+//     that stream the keys one after the other, each a head of its own in the tile lists.
 //   * The K scale enters with the softmax scale; the V scale enters the exponent: p' = 2^(x + log2 s -
 //     m), O sums p' u, and the normaliser sums p' / s.  So a block costs no multiply of its own per
 //     element, and the reference m follows the size of p' u, which is what O accumulates.
@@ -42,32 +48,50 @@ constexpr float kScoreHi = 15.f, kScoreLo = 7.f;
 // per 64-key block, TG tile groups consuming alternate tiles.
 template <int D, int NQT, int WR, int WK, int TG, bool Q8>
 struct SCfg {
+    static constexpr bool WIDE = NQT >= 4;  // keys and head_dim split over the warps of a group
+    static_assert(!WIDE || (WR == 1 && WK == 4), "a wide group is four warps");
     static constexpr int NQ = 8 * NQT;
     static constexpr int ROWS = NQ * WR;
     static constexpr int GW = WR * WK;
     static constexpr int NCW = GW * TG;
+    static constexpr int NP = WK * TG;  // warps that share a query row
     // with two query tiles per warp the producer warp heads a warpgroup that gives registers up
-    static constexpr bool SPLIT = NQT >= 2;
+    static constexpr bool SPLIT = NQT == 2;
     static constexpr int THREADS = SPLIT ? (NCW + 4) * 32 : (NCW + 1) * 32;
     static constexpr int LAUNCH_REGS = (65536 / THREADS) / 8 * 8 > 255 ? 248 : (65536 / THREADS) / 8 * 8;
     static constexpr int REG_PRODUCER = 72;
     static constexpr int REG_FREE = ((LAUNCH_REGS * (NCW + 4) - 4 * REG_PRODUCER) / NCW) / 8 * 8;
     static constexpr int REG_CONSUMER = REG_FREE > 248 ? 248 : REG_FREE;
-    static_assert(NCW % 4 == 0, "consumer warps form whole warpgroups");
-    static_assert(NCW * REG_CONSUMER + 4 * REG_PRODUCER <= (NCW + 4) * LAUNCH_REGS, "register split");
+    static_assert(WIDE || NCW % 4 == 0, "consumer warps form whole warpgroups");
+    static_assert(!SPLIT || NCW * REG_CONSUMER + 4 * REG_PRODUCER <= (NCW + 4) * LAUNCH_REGS, "register split");
     static constexpr int SB = 4 / WK;  // 16-key sub-blocks per warp and block
+    static constexpr int MT = WIDE ? (D == 64 ? 1 : 2) : D / 16;  // 16-column tiles of O per warp
     static constexpr int NBOX = D / kBoxCols;
-    static constexpr int STAGE_BYTES = Q8 ? (2 * q8_record_bytes(D) + 1023) / 1024 * 1024 : 2 * NBOX * kBoxBytes;
-    static_assert(STAGE_BYTES >= 2 * NBOX * kBoxBytes, "a stage holds a bf16 tile too");
+    static constexpr int BOX_ROWS = WIDE && Q8 ? kWideRingRows : kTileRows;  // rows of a ring tile's boxes
+    static constexpr int RING_BYTES = 2 * NBOX * BOX_ROWS * 64;
+    static constexpr int DEEP_BYTES = Q8 ? (WIDE ? 1 : 2) * q8_record_bytes(D) : RING_BYTES;
+    // a multiple of the 64-byte swizzle's 512-byte period
+    static constexpr int STAGE_BYTES = ((DEEP_BYTES > RING_BYTES ? DEEP_BYTES : RING_BYTES) + 511) / 512 * 512;
+    // Q in fragment order, [form][row tile][D / 32][lane] of 16 bytes: bf16, and f16 for 8-bit tiles
+    static constexpr int QF_BYTES = ROWS * D * 2;
+    static constexpr int Q_BYTES = (Q8 ? 2 : 1) * QF_BYTES;
+    // WIDE: P in fragment order, [group][2][16-key sub-block][pair of row tiles][lane] of 16 bytes
+    static constexpr int P_BYTES = WIDE ? TG * 2 * 4 * (NQT / 2) * 512 : 0;
+    // merge buffer: rows of o per warp, or per group of a wide one; (m, l_out, l_lse) per warp
     static constexpr int DP = D + 4;
-    static constexpr int MERGE_FLOATS = NCW * NQ * DP;
-    static constexpr int MLF = NCW * NQ * 4 + ROWS * (TG * WK + 4);
+    static constexpr int SLOTS = WIDE ? TG : NCW;
+    static constexpr int NPF = WIDE ? TG : NP;  // partials of a row of o
+    static constexpr int MERGE_FLOATS = SLOTS * NQ * DP;
+    static constexpr int GM_FLOATS = WIDE ? NCW * NQ : 0;  // column maxima of a wide group's warps
+    static constexpr int MLF = NCW * NQ * 4 + ROWS * (NPF + 4) + 3 * ROWS + GM_FLOATS + (WIDE ? 4 * TG : 0);
+    static_assert(MLF % 4 == 0 && (ROWS * NPF) % 4 == 0, "alignment");
     static constexpr int MISC = 1024 + 1024;
-    static constexpr int AVAIL = kSmemLimit - MISC - 4 * (MERGE_FLOATS + MLF) - 4 * (2 * kMaxBatch + 2);
+    static constexpr int AVAIL =
+        kSmemLimit - MISC - Q_BYTES - P_BYTES - 4 * (MERGE_FLOATS + MLF) - 4 * (2 * kMaxBatch + 2);
     static constexpr int NS_RAW = AVAIL / STAGE_BYTES > 8 ? 8 : AVAIL / STAGE_BYTES;
     static constexpr int NS = NS_RAW - NS_RAW % TG;  // a stage always serves the same tile group
     static_assert(NS >= 2, "not enough shared memory for the pipeline");
-    static constexpr int SMEM_FIXED = MISC + NS * STAGE_BYTES + 4 * (MERGE_FLOATS + MLF);
+    static constexpr int SMEM_FIXED = MISC + Q_BYTES + P_BYTES + NS * STAGE_BYTES + 4 * (MERGE_FLOATS + MLF);
     static_assert(SMEM_FIXED + 4 * (2 * kMaxBatch + 2) <= kSmemLimit, "shared memory");
     static constexpr int MAX_PARTS =
         (NS * STAGE_BYTES) / (2 * ROWS * 4) < 256 ? (NS * STAGE_BYTES) / (2 * ROWS * 4) : 256;
@@ -81,6 +105,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -90,12 +124,26 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// D = A * B (+ D): f16 or bf16 operands, fp32 sums; the first product of a chain needs no zeroed registers
+template <bool HALF, bool FIRST>
+__device__ __forceinline__ void mma_step(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (FIRST && HALF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%10, %10, %10, %10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else if constexpr (FIRST)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%10, %10, %10, %10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else if constexpr (HALF)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        mma_16816(d, a, b0, b1);
 }
 
 // four bytes u + 128 -> two pairs of f16 u: (bytes 0, 1) and (bytes 2, 3)
@@ -120,7 +168,7 @@ struct ScoreChunk {
 
 __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum, int *Ts, int *sflag, int tid, int warp,
                                                    int lane) {
-    const int N = a.N, kvH = a.kvH;
+    const int N = a.N, kvH = a.kvH * a.groups;
     ScoreChunk c;
     for (int n = tid; n < N; n += blockDim.x) {
         const int T = a.T[n];
@@ -180,10 +228,17 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     extern __shared__ uint8_t smem_raw[];
     uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                   ~static_cast<uintptr_t>(1023));
-    float *mo = reinterpret_cast<float *>(stages + NS * C::STAGE_BYTES);  // [NCW][NQ][DP]
+    uint8_t *qf = stages + NS * C::STAGE_BYTES;                           // Q fragments, then P (WIDE)
+    float *mo = reinterpret_cast<float *>(qf + C::Q_BYTES + C::P_BYTES);  // [SLOTS][NQ][DP]
     float *mml = mo + C::MERGE_FLOATS;                                    // [NCW][NQ][4] m, l_out, l_lse
-    float *wq = mml + C::NCW * C::NQ * 4;                                 // [ROWS][TG*WK] weights
-    float *fin = wq + C::ROWS * TG * WK;                                  // [ROWS][4] final m, l_out, l_lse
+    float *wq = mml + C::NCW * C::NQ * 4;                                 // [ROWS][NPF] weights
+    float *fin = wq + C::ROWS * C::NPF;                                   // [ROWS][4] final m, l_out, l_lse
+    float *qscale = fin + C::ROWS * 4;                                    // [ROWS] sx over the row's power of two
+    float *qslope = qscale + C::ROWS;                                     // [ROWS] distance bias of the row's head
+    int *qpos = reinterpret_cast<int *>(qslope + C::ROWS);                // [ROWS] block position, -1: no such row
+    float *gmax = reinterpret_cast<float *>(qpos + C::ROWS);              // [NCW][NQ] column maxima (WIDE)
+    // WIDE [TG][4]: the last even and the last odd block that moves a reference; the group has given up; -
+    int *gflag = reinterpret_cast<int *>(gmax + C::GM_FLOATS);
     uint64_t *bars = reinterpret_cast<uint64_t *>(mml + C::MLF);          // full[NS], empty[NS]
     TileDesc *sdesc = reinterpret_cast<TileDesc *>(bars + 2 * NS);        // [NS]
     int *sflag = reinterpret_cast<int *>(sdesc + NS);                     // [16]
@@ -194,7 +249,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     const int warp = tid >> 5;
     const int lane = tid & 31;
     const ScorePlan &pa = a.plan;
-    const int N = a.N, kvH = a.kvH;
+    const int N = a.N, kvH = a.kvH * a.groups;  // each row group of a kv head counts as a head
 
     if (warp == C::NCW && lane == 0) {
         tma_prefetch_desc(&tmKw);
@@ -213,12 +268,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         }
         mbar_fence_init();
     }
-    // rows past a short box are never written by TMA: keep them finite
-    if (pa.deep_box < kTileRows || pa.ring_box < kTileRows) {
-        uint4 *z = reinterpret_cast<uint4 *>(stages);
-        for (int i = tid; i < NS * C::STAGE_BYTES / 16; i += blockDim.x) z[i] = make_uint4(0, 0, 0, 0);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    }
+    if (C::WIDE && tid < 4 * TG) gflag[tid] = -1;
     if (!a.early) pdl_wait();
     const ScoreChunk cp = score_chunks(a, cum, Ts, sflag, tid, warp, lane);
     const int chunk = cp.chunk, pieces = cp.pieces;
@@ -265,20 +315,20 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             }
             if (Q8 && deep) {
                 const uint32_t bytes = static_cast<uint32_t>(t.cnt >> 6) * q8_record_bytes(D);
-                const size_t r = (static_cast<size_t>(a.layer) * N + n) * kvH + kh;
+                const size_t r = (static_cast<size_t>(a.layer) * N + n) * a.kvH + kh / a.groups;
                 mbar_expect_tx(fb, bytes);
                 bulk_load(kdst, a.rec + (r * a.rec_blocks + (t.t0 >> 6)) * q8_record_bytes(D), bytes, fb);
             } else {
                 const int rows = deep ? pa.deep_box : pa.ring_box;
                 const CUtensorMap *mk = deep ? &tmKd : &tmKw;
                 const CUtensorMap *mv = deep ? &tmVd : &tmVw;
-                const int z = deep ? ((a.layer * N + n) * kvH + kh) : (((a.layer * N + n) * pa.R + t.plane) * kvH + kh);
-                const uint32_t vdst = kdst + C::NBOX * kBoxBytes;
+                const int z = (deep ? a.layer * N + n : (a.layer * N + n) * pa.R + t.plane) * a.kvH + kh / a.groups;
+                const uint32_t vdst = kdst + C::RING_BYTES / 2;
                 mbar_expect_tx(fb, 2 * C::NBOX * rows * 64);
 #pragma unroll
                 for (int b = 0; b < C::NBOX; ++b) {
-                    tma_load_3d(kdst + b * kBoxBytes, mk, fb, b * kBoxCols, t.y, z);
-                    tma_load_3d(vdst + b * kBoxBytes, mv, fb, b * kBoxCols, t.y, z);
+                    tma_load_3d(kdst + b * C::BOX_ROWS * 64, mk, fb, b * kBoxCols, t.y, z);
+                    tma_load_3d(vdst + b * C::BOX_ROWS * 64, mv, fb, b * kBoxCols, t.y, z);
                 }
             }
             if (++lt == sg.total) {
@@ -304,16 +354,9 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     const int kg = warp % WK;            // sub-blocks kg*SB .. kg*SB + SB-1
     const int g4 = lane >> 2, c4 = lane & 3;
     const int nct = C::NCW * 32;
+    // a thread holds the query columns NQ*rg + 8*nq + 2*c4 + e
+    const int col0 = C::NQ * rg + 2 * c4;
 
-    // query columns held by this thread: NQ*rg + 8*nq + 2*c4 + e
-    int jq[NQT][2];
-#pragma unroll
-    for (int nq = 0; nq < NQT; ++nq)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = C::NQ * rg + 8 * nq + 2 * c4 + e;
-            jq[nq][e] = i < a.Mq ? pa.j0 + i / a.g : -1;
-        }
     // ldmatrix lane geometry of the bf16 tiles (64-byte swizzle: 16-byte chunk ^= (row >> 1) & 3)
     const int mi = lane >> 3, r8 = lane & 7;
     const uint32_t swz = static_cast<uint32_t>(r8 >> 1);
@@ -321,87 +364,86 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     const uint32_t kcol_sel = static_cast<uint32_t>(mi >> 1);
     const uint32_t vrow_off = static_cast<uint32_t>((mi >> 1) * 8 + r8);
     const uint32_t vcol_sel = static_cast<uint32_t>(mi & 1);
+    // this lane's Q fragments of row tile NQT*rg
+    const uint32_t qf0 = smem_addr(qf) + NQT * rg * (D / 32) * 512 + lane * 16;
 
-    float o[D / 16][NQT][4];
-    // l_lse sums the probabilities in fp32, l_out as the P V product of a bf16 tile sees them (rounded)
+    float o[C::MT][NQT][4];
+    // l_lse sums the probabilities in fp32, l_out as the P V product of a bf16 tile sees them (rounded);
+    // a column's reference means nothing until some lane's l_lse is not zero
     float m_ref[NQT][2], l_lse[NQT][2], l_out[NQT][2];
-    uint32_t qb[D / 16][NQT][2];  // Q as B fragments: bf16, or f16 in the column order of 8-bit tiles
-    float fcol[NQT][2];           // 8-bit tiles: sx over the power of two that scaled the row
-    float slope[NQT][2];          // distance bias of the column's head
+    uint32_t seen = 0;  // WIDE: bit 2 nq + e is set once the column has a reference
+    uint32_t qb[C::WIDE ? 1 : D / 16][C::WIDE ? 1 : NQT][2];  // Q as B fragments
 
-    int fin_next = P_first;
-    int st_pair = -1;
-    bool st_half = false;  // qb holds the f16 form
+    int st_pair = P_first;
+    int st_half = -1;  // qb holds the f16 (1) or bf16 (0) form
     bool aborted = false;
 
     auto reset_state = [&]() {
+        seen = 0;
 #pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt)
+        for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
             for (int nq = 0; nq < NQT; ++nq) o[mt][nq][0] = o[mt][nq][1] = o[mt][nq][2] = o[mt][nq][3] = 0.f;
 #pragma unroll
         for (int nq = 0; nq < NQT; ++nq) {
-            m_ref[nq][0] = m_ref[nq][1] = -INFINITY;
+            m_ref[nq][0] = m_ref[nq][1] = 0.f;
             l_lse[nq][0] = l_lse[nq][1] = 0.f;
             l_out[nq][0] = l_out[nq][1] = 0.f;
         }
     };
 
-    auto load_q = [&](int n, int kh, bool half) {
-        st_half = half;
+    // kv head of pair p, its first query row, and how many rows the pair has
+    auto head_of = [&](int p) { return (p % kvH) / a.groups; };
+    auto group_row = [&](int p) { return (p % kvH) % a.groups * a.grows; };
+    auto rows_of = [&](int p) { return min(a.grows, a.Mq - group_row(p)); };
+
+    // All consumer warps: Q of pair p into shared memory, in fragment order.  bf16: of each 16 columns, lane
+    // (g4, c4) has 2 c4, 2 c4 + 1 and 8 more; f16: 4 c4 .. 4 c4 + 3, the order of the 8-bit K fragments.
+    auto stage_q = [&](int p) {
+        for (int i = warp; i < C::ROWS; i += C::NCW) {
+            uint32_t w[(D + 63) / 64];
+            const int h = head_of(p), row = group_row(p) + i;
+            const bool have = i < rows_of(p);
+            const int j = have ? row / a.g : 0, hg = have ? row - j * a.g : 0;
+            const uint32_t *qp = reinterpret_cast<const uint32_t *>(
+                a.q + ((static_cast<size_t>(p / kvH) * a.qB + j) * a.Hq + h * a.g + hg) * D);
+            if (lane == 0) qpos[i] = have ? pa.j0 + j : -1;
+            uint32_t most = 0;  // largest magnitude of the row, as bf16 bits
 #pragma unroll
-        for (int nq = 0; nq < NQT; ++nq) {
-            const int i = C::NQ * rg + 8 * nq + g4;  // B-operand column = query g4 of the tile
-            const uint32_t *qp = nullptr;
-            if (i < a.Mq) {
-                const int j = i / a.g, hg = i - j * a.g;
-                qp = reinterpret_cast<const uint32_t *>(
-                    a.q + ((static_cast<size_t>(n) * a.qB + j) * a.Hq + kh * a.g + hg) * D);
+            for (int u = 0; u < (D + 63) / 64; ++u) {
+                const bool in = have && u * 32 + lane < D / 2;
+                w[u] = in ? __ldg(qp + u * 32 + lane) : 0u;
+                most = max(most, max(w[u] & 0x7FFFu, (w[u] >> 16) & 0x7FFFu));
             }
-            if (Q8 && half) {
-                uint32_t most = 0;  // largest magnitude of the row, as bf16 bits
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    uint2 w = make_uint2(0, 0);
-                    if (qp) w = __ldg(reinterpret_cast<const uint2 *>(qp + 8 * ks + 2 * c4));
-                    qb[ks][nq][0] = w.x;
-                    qb[ks][nq][1] = w.y;
-                    most = max(most, max(max(w.x & 0x7FFFu, (w.x >> 16) & 0x7FFFu),
-                                         max(w.y & 0x7FFFu, (w.y >> 16) & 0x7FFFu)));
-                }
-                most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            float up = 1.f;
+            if constexpr (Q8) {
+                most = __reduce_max_sync(0xffffffffu, most);
                 // 2^k that brings the row's largest element into [16, 32); 1 for a row with infinities or NaN
                 const int ex = static_cast<int>(most >> 7);
                 const int k = ex == 255 ? 0 : min(131 - ex, 126);
-                const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t w = qb[ks][nq][x];
-                        const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * up,
-                                                            __uint_as_float(w & 0xFFFF0000u) * up);
-                        qb[ks][nq][x] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) fcol[nq][e] = a.sx * __shfl_sync(0xffffffffu, down, (2 * c4 + e) * 4);
-            } else {
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    qb[ks][nq][0] = qp ? __ldg(qp + 8 * ks + c4) : 0u;
-                    qb[ks][nq][1] = qp ? __ldg(qp + 8 * ks + 4 + c4) : 0u;
-                }
+                up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+                if (lane == 0) qscale[i] = a.sx * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
             }
-            if (MOD) {
+            if (MOD && lane == 0)
+                qslope[i] = a.slopes && have ? __ldg(a.slopes + h * a.g + hg) * 1.4426950408889634f : 0.f;
+            uint8_t *dst = qf + (i >> 3) * (D / 32) * 512 + (i & 7) * 64;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int ic = C::NQ * rg + 8 * nq + 2 * c4 + e;
-                    slope[nq][e] = a.slopes && ic < a.Mq ? __ldg(a.slopes + kh * a.g + ic % a.g) * 1.4426950408889634f : 0.f;
+            for (int u = 0; u < (D + 63) / 64; ++u) {
+                const int at = u * 32 + lane, ks = at >> 3, x = at & 7;  // columns 2 at, 2 at + 1
+                if (at < D / 2) {
+                    uint8_t *f = dst + (ks >> 1) * 512 + (ks & 1) * 8;
+                    *reinterpret_cast<uint32_t *>(f + (x & 3) * 16 + (x >> 2) * 4) = w[u];
+                    if constexpr (Q8) {
+                        const __half2 h = __floats2half2_rn(__uint_as_float(w[u] << 16) * up,
+                                                            __uint_as_float(w[u] & 0xFFFF0000u) * up);
+                        *reinterpret_cast<uint32_t *>(f + C::QF_BYTES + (x >> 1) * 16 + (x & 1) * 4) =
+                            *reinterpret_cast<const uint32_t *>(&h);
+                    }
                 }
             }
         }
+        st_half = -1;
+        named_bar_sync(1, nct);
     };
 
     // the CTAs holding tiles of pair p: c_first .. c_first + nparts - 1 (returns nparts)
@@ -419,10 +461,9 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
 
     // four columns of the output of row i (block position, head) of pair p, and its log-sum-exp
     auto write_row = [&](int p, int i, int c0, float4 acc, float m, float lo, float ll) {
-        const int n = p / kvH, kh = p - (p / kvH) * kvH;
         const float inv = 1.f / lo;
-        const int j = i / a.g, h = kh * a.g + (i - j * a.g);
-        const size_t orow = (static_cast<size_t>(n) * a.qB + j) * a.Hq + h;
+        const int row = group_row(p) + i, j = row / a.g, h = head_of(p) * a.g + (row - j * a.g);
+        const size_t orow = (static_cast<size_t>(p / kvH) * a.qB + j) * a.Hq + h;
         __nv_bfloat162 *op = reinterpret_cast<__nv_bfloat162 *>(&a.out[orow * D + c0]);
         op[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
         op[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
@@ -430,24 +471,14 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     };
 
     // ---------------------------------------------------------------- finalize one pair
+    // Every consumer warp, for every pair of the CTA in order; then Q of the next pair is staged.
     auto finalize = [&](int p, bool have) {
-        float *mw = mo + warp * C::NQ * C::DP;
-        if (have) {
+        const int slot = (tg * WK + kg) * WR + rg;  // this warp's (m, l)
+        if (!have) reset_state();
+        if (!C::WIDE || 16 * C::MT * kg < D) {
+            float *mw = mo + (C::WIDE ? tg : slot) * C::NQ * C::DP + (C::WIDE ? 16 * C::MT * kg : 0);
 #pragma unroll
-            for (int nq = 0; nq < NQT; ++nq)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float l = l_lse[nq][e], lb = l_out[nq][e];
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) {
-                        l += __shfl_xor_sync(0xffffffffu, l, x);
-                        lb += __shfl_xor_sync(0xffffffffu, lb, x);
-                    }
-                    l_lse[nq][e] = l;
-                    l_out[nq][e] = lb;
-                }
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt)
+            for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
                 for (int nq = 0; nq < NQT; ++nq) {
                     const int q0 = 8 * nq + 2 * c4;
@@ -456,18 +487,22 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                     mw[q0 * C::DP + 16 * mt + 8 + g4] = o[mt][nq][2];
                     mw[(q0 + 1) * C::DP + 16 * mt + 8 + g4] = o[mt][nq][3];
                 }
-            if (g4 == 0) {
-#pragma unroll
-                for (int nq = 0; nq < NQT; ++nq)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float4 *>(&mml[(warp * C::NQ + 8 * nq + 2 * c4 + e) * 4]) =
-                            make_float4(m_ref[nq][e], l_out[nq][e], l_lse[nq][e], 0.f);
-            }
-        } else {
-            for (int q = lane; q < C::NQ; q += 32)
-                *reinterpret_cast<float4 *>(&mml[(warp * C::NQ + q) * 4]) = make_float4(-INFINITY, 0.f, 0.f, 0.f);
         }
+#pragma unroll
+        for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = l_lse[nq][e], lb = l_out[nq][e];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    l += __shfl_xor_sync(0xffffffffu, l, x);
+                    lb += __shfl_xor_sync(0xffffffffu, lb, x);
+                }
+                const bool none = C::WIDE ? !(seen >> (2 * nq + e) & 1) : l == 0.f;  // (the same for a wide group)
+                if (g4 == 0)
+                    *reinterpret_cast<float4 *>(&mml[(slot * C::NQ + 8 * nq + 2 * c4 + e) * 4]) =
+                        make_float4(none ? -INFINITY : m_ref[nq][e], lb, l, 0.f);
+            }
         named_bar_sync(1, nct);
         const bool abort_now = *reinterpret_cast<volatile int *>(&sflag[1]) != 0;
         int c_first;
@@ -477,16 +512,13 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             const int rgi = i / C::NQ, q = i - rgi * C::NQ;
             float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < TG * WK; ++w)
-                M = fmaxf(M, mml[(((w / WK) * C::GW + rgi * WK + w % WK) * C::NQ + q) * 4]);
+            for (int w = 0; w < C::NP; ++w) M = fmaxf(M, mml[((w * WR + rgi) * C::NQ + q) * 4]);
             float L = 0.f, Ll = 0.f;
 #pragma unroll
-            for (int w = 0; w < TG * WK; ++w) {
-                const float4 ml = *reinterpret_cast<const float4 *>(
-                    &mml[(((w / WK) * C::GW + rgi * WK + w % WK) * C::NQ + q) * 4]);
-                // a partial without a reference has no sums, or NaN of a block that reads as NaN
-                const float f = ml.x == -INFINITY ? (ml.z == 0.f ? 0.f : ml.z) : exp2f(ml.x - M);
-                wq[i * (TG * WK) + w] = f;
+            for (int w = 0; w < C::NP; ++w) {
+                const float4 ml = *reinterpret_cast<const float4 *>(&mml[((w * WR + rgi) * C::NQ + q) * 4]);
+                const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+                if (!C::WIDE || w % WK == 0) wq[i * C::NPF + (C::WIDE ? w / WK : w)] = f;
                 L += f * ml.y;
                 Ll += f * ml.z;
             }
@@ -494,17 +526,16 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         }
         named_bar_sync(1, nct);
         constexpr int D4 = D / 4;
-        const int rows = sole ? a.Mq : C::ROWS;
+        const int rows = sole ? rows_of(p) : C::ROWS;
         for (int e = tid; e < rows * D4 && !abort_now; e += nct) {
             const int i = e / D4, c0 = 4 * (e - i * D4);
             const int rgi = i / C::NQ, q = i - rgi * C::NQ;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < TG * WK; ++w) {
-                const float f = wq[i * (TG * WK) + w];
+            for (int w = 0; w < C::NPF; ++w) {
+                const float f = wq[i * C::NPF + w];
                 if (f != 0.f) {
-                    const float4 v = *reinterpret_cast<const float4 *>(
-                        &mo[(((w / WK) * C::GW + rgi * WK + w % WK) * C::NQ + q) * C::DP + c0]);
+                    const float4 v = *reinterpret_cast<const float4 *>(&mo[((w * WR + rgi) * C::NQ + q) * C::DP + c0]);
                     acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
                 }
             }
@@ -531,42 +562,45 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                 sflag[3] += 1;
             }
         }
+        if (p < P_last) {
+            stage_q(p + 1);
+            reset_state();
+        }
     };
 
     // ---------------------------------------------------------------- merge the partials of one pair
     // Runs in the CTA that arrived last, after all of its own tiles (the stage buffers are free).
     auto merge_pair = [&](int p) {
         int c_first;
-        const int nparts = parts_of(p, c_first);
+        const int nparts = parts_of(p, c_first), mq = rows_of(p);
         float *pw = reinterpret_cast<float *>(stages);  // [nparts][ROWS] m, then weights
         float *pl = pw + nparts * C::ROWS;              // [nparts][ROWS] l
-        for (int e = tid; e < nparts * a.Mq; e += nct) {
-            const int c = e / a.Mq, i = e - (e / a.Mq) * a.Mq;
+        for (int e = tid; e < nparts * mq; e += nct) {
+            const int c = e / mq, i = e - (e / mq) * mq;
             const size_t prow = (static_cast<size_t>(c_first + c) + p) * C::ROWS + i;
             const float2 ml = __ldcg(reinterpret_cast<const float2 *>(&a.part_ml[prow * 4]));
             pw[c * C::ROWS + i] = ml.x;
             pl[c * C::ROWS + i] = ml.y;
         }
         named_bar_sync(1, nct);
-        for (int i = tid; i < a.Mq; i += nct) {
+        for (int i = tid; i < mq; i += nct) {
             float M = -INFINITY;
             for (int c = 0; c < nparts; ++c) M = fmaxf(M, pw[c * C::ROWS + i]);
             float L = 0.f, Ll = 0.f;
             for (int c = 0; c < nparts; ++c) {
                 const float mk = pw[c * C::ROWS + i];
                 const size_t prow = (static_cast<size_t>(c_first + c) + p) * C::ROWS + i;
-                const float ll = __ldcg(&a.part_ml[prow * 4 + 2]);
-                const float w = mk == -INFINITY ? (ll == 0.f ? 0.f : ll) : exp2f(mk - M);
+                const float w = mk == -INFINITY ? 0.f : exp2f(mk - M);
                 pw[c * C::ROWS + i] = w;
                 L += w * pl[c * C::ROWS + i];
-                Ll += w * ll;
+                Ll += w * __ldcg(&a.part_ml[prow * 4 + 2]);
             }
             fin[i * 4] = M;
             fin[i * 4 + 1] = L;
             fin[i * 4 + 2] = Ll;
         }
         named_bar_sync(1, nct);
-        for (int e = tid; e < a.Mq * (D / 4); e += nct) {
+        for (int e = tid; e < mq * (D / 4); e += nct) {
             const int i = e / (D / 4), cx = e - (e / (D / 4)) * (D / 4);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -582,264 +616,440 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         named_bar_sync(1, nct);
     };
 
-    // ---------------------------------------------------------------- 64 keys of one tile
-    // kb0: shared-memory address of the keys (a bf16 tile or an 8-bit record); t0, cnt: first key, keys
-    auto compute = [&](const TileDesc &dsc, uint32_t kb0, int t0, int cnt, auto fast_tag, auto half_tag) {
-        constexpr bool FAST = decltype(fast_tag)::value;   // every query sees all 64 keys
-        constexpr bool HALF = decltype(half_tag)::value;   // an 8-bit block
-        const uint32_t vb0 = kb0 + (HALF ? 64 * D : C::NBOX * kBoxBytes);
-        float x[C::SB][NQT][4];
-        bool act[C::SB];
-        float ks = 1.f, lv = 0.f, iv = 1.f;
-        if constexpr (HALF) {
-            const uint4 sc = lds128(kb0 + 128 * D);
-            ks = __uint_as_float(sc.x);
-            lv = __uint_as_float(sc.y);
-            iv = __uint_as_float(sc.z);
-        }
-#pragma unroll
-        for (int sb = 0; sb < C::SB; ++sb) {
-            const int kb = kg * C::SB + sb;
-            act[sb] = FAST || 16 * kb < cnt;
-            float se[NQT][4], so[NQT][4];
+    // Q fragments of columns 32 kp .. + 31 of query tile nq: k-steps 2 kp and 2 kp + 1
+    auto q_frag = [&](int kp, int nq, bool half) -> uint4 {
+        return lds128(qf0 + (half ? C::QF_BYTES : 0) + (nq * (D / 32) + kp) * 512);
+    };
+    auto load_q = [&](bool half) {
+        if constexpr (!C::WIDE) {
 #pragma unroll
             for (int nq = 0; nq < NQT; ++nq)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) se[nq][e] = so[nq][e] = 0.f;
-            if (act[sb]) {
-                if constexpr (HALF) {
-#pragma unroll
-                    for (int kp = 0; kp < D / 32; ++kp) {
-                        const uint4 w = lds128(kb0 + kb * 16 * D + (kp * 32 + lane) * 16);
-                        uint32_t af[4];
-                        q8_to_f16(w.x, af[0], af[2]);
-                        q8_to_f16(w.y, af[1], af[3]);
-#pragma unroll
-                        for (int nq = 0; nq < NQT; ++nq) mma_16816_f16(se[nq], af, qb[2 * kp][nq][0], qb[2 * kp][nq][1]);
-                        q8_to_f16(w.z, af[0], af[2]);
-                        q8_to_f16(w.w, af[1], af[3]);
-#pragma unroll
-                        for (int nq = 0; nq < NQT; ++nq)
-                            mma_16816_f16(so[nq], af, qb[2 * kp + 1][nq][0], qb[2 * kp + 1][nq][1]);
-                    }
-                } else {
-                    const uint32_t krow = static_cast<uint32_t>(16 * kb) + krow_off;
-#pragma unroll
-                    for (int ks2 = 0; ks2 < D / 16; ++ks2) {
-                        const uint32_t col16 = static_cast<uint32_t>(2 * (ks2 & 1)) + kcol_sel;
-                        uint32_t af[4];
-                        ldsm_x4(kb0 + (ks2 >> 1) * kBoxBytes + krow * 64 + ((col16 ^ swz) << 4), af[0], af[1], af[2], af[3]);
-#pragma unroll
-                        for (int nq = 0; nq < NQT; ++nq) {
-                            if (ks2 & 1) mma_16816(so[nq], af, qb[ks2][nq][0], qb[ks2][nq][1]);
-                            else mma_16816(se[nq], af, qb[ks2][nq][0], qb[ks2][nq][1]);
-                        }
-                    }
+                for (int kp = 0; kp < D / 32; ++kp) {
+                    const uint4 w = q_frag(kp, nq, half);
+                    qb[2 * kp][nq][0] = w.x;
+                    qb[2 * kp][nq][1] = w.y;
+                    qb[2 * kp + 1][nq][0] = w.z;
+                    qb[2 * kp + 1][nq][1] = w.w;
                 }
+        }
+        st_half = half ? 1 : 0;
+    };
+
+    // ---------------------------------------------------------------- one block of keys, in pieces
+    // kb0: shared-memory address of the keys (a bf16 tile or an 8-bit record); t0, cnt: first key, keys.
+    // FAST: every query sees all 64 keys; HALF: an 8-bit block.
+    constexpr uint32_t kBox = C::BOX_ROWS * 64;  // bytes of a box
+    struct Scales { float ks, lv, iv; };         // of an 8-bit block: K scale, log2 of the V scale and 1 / it
+    auto scales_of = [&](uint32_t kb0) -> Scales {
+        const uint4 sc = lds128(kb0 + 128 * D);
+        return {__uint_as_float(sc.x), __uint_as_float(sc.y), __uint_as_float(sc.z)};
+    };
+
+    // S^T of 16 keys (sub-block kb) and this warp's query columns
+    auto scores = [&](uint32_t kb0, int kb, float (&x)[NQT][4], auto half_tag) {
+        constexpr bool HALF = decltype(half_tag)::value;
+#pragma unroll
+        for (int kp = 0; kp < D / 32; ++kp) {
+            uint32_t a0[4], a1[4];  // K of k-steps 2 kp, 2 kp + 1
+            if constexpr (HALF) {
+                const uint4 w = lds128(kb0 + kb * 16 * D + (kp * 32 + lane) * 16);
+                q8_to_f16(w.x, a0[0], a0[2]);
+                q8_to_f16(w.y, a0[1], a0[3]);
+                q8_to_f16(w.z, a1[0], a1[2]);
+                q8_to_f16(w.w, a1[1], a1[3]);
+            } else {
+                const uint32_t row = kb0 + kp * kBox + (static_cast<uint32_t>(16 * kb) + krow_off) * 64;
+                ldsm_x4(row + ((kcol_sel ^ swz) << 4), a0[0], a0[1], a0[2], a0[3]);
+                ldsm_x4(row + (((2 + kcol_sel) ^ swz) << 4), a1[0], a1[1], a1[2], a1[3]);
             }
 #pragma unroll
-            for (int nq = 0; nq < NQT; ++nq)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float f = HALF ? ks * fcol[nq][e & 1] : a.sx;
-                    float v = se[nq][e] + so[nq][e];
-                    const int kk = 16 * kb + g4 + 8 * (e >> 1);
-                    if (MOD && a.cap != 0.f)
-                        v = fmaf(-2.f * a.cap, __fdividef(1.f, 1.f + exp2f(v * f)), a.cap + lv);
-                    else
-                        v = HALF ? fmaf(v, f, lv) : v * f;
-                    if (MOD) v = fmaf(slope[nq][e & 1], static_cast<float>(t0 + kk - (dsc.T + jq[nq][e & 1])), v);
-                    if (!FAST) {
-                        const int j = jq[nq][e & 1];
-                        const bool vis = j >= 0 && act[sb] && kk < cnt &&
-                                         score_sees(pa, dsc.T, dsc.kind, dsc.plane, t0 + kk, j, pa.jloop[j < 0 ? 0 : j]);
-                        v = vis ? v : -INFINITY;
-                    }
-                    x[sb][nq][e] = v;
-                }
+            for (int nq = 0; nq < NQT; ++nq) {
+                uint4 b;
+                if constexpr (C::WIDE) b = q_frag(kp, nq, HALF);
+                else b = make_uint4(qb[2 * kp][nq][0], qb[2 * kp][nq][1], qb[2 * kp + 1][nq][0], qb[2 * kp + 1][nq][1]);
+                if (kp == 0) mma_step<HALF, true>(x[nq], a0, b.x, b.y);
+                else mma_step<HALF, false>(x[nq], a0, b.x, b.y);
+                mma_step<HALF, false>(x[nq], a1, b.z, b.w);
+            }
         }
-        // the reference of a column moves when the warp's maximum exceeds it by more than kScoreHi, which
-        // is so exactly when one lane's own maximum does
-        bool over = false;
-        float mloc[NQT][2];
+    };
+
+    // Dot products of SB sub-blocks (the first is sub-block kb1) to scores relative to the column's reference, in
+    // log2 units (8-bit: + log2 of the V scale); what a query does not see to -infinity.
+    auto relative = [&](const TileDesc &dsc, int t0, int cnt, int kb1, const Scales &sc, float (&x)[C::SB][NQT][4],
+                        auto fast_tag, auto half_tag) {
+        constexpr bool FAST = decltype(fast_tag)::value, HALF = decltype(half_tag)::value;
 #pragma unroll
         for (int nq = 0; nq < NQT; ++nq)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float mt = -INFINITY;
-#pragma unroll
-                for (int sb = 0; sb < C::SB; ++sb) mt = fmaxf(mt, fmaxf(x[sb][nq][e], x[sb][nq][e + 2]));
-                mloc[nq][e] = mt;
-                over = over || mt > m_ref[nq][e] + kScoreHi;
-            }
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-            for (int nq = 0; nq < NQT; ++nq) {
-                float al[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mt = mloc[nq][e];
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 4));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 8));
-                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
-                    al[e] = 1.f;
-                    if (mt > m_ref[nq][e] + kScoreHi) {
-                        al[e] = exp2f(m_ref[nq][e] - (mt - kScoreLo));
-                        m_ref[nq][e] = mt - kScoreLo;
+                const int col = col0 + 8 * nq + e;
+                const int jq = FAST && !MOD ? 0 : qpos[col];
+                const float f = HALF ? sc.ks * qscale[col] : a.sx;
+                const float off = HALF ? sc.lv - m_ref[nq][e] : -m_ref[nq][e];
+                // distance of this lane's first key from the query (exact below 2^24), and its visible range
+                const int first = t0 + 16 * kb1 + g4;
+                const float slope = MOD ? qslope[col] : 0.f;
+                const float dist = MOD ? static_cast<float>(first - (dsc.T + jq)) : 0.f;
+                int lo = 0, hi = 0, sink = 0, win = 0;
+                if (!FAST && jq >= 0) {
+                    score_range(pa, dsc.T, dsc.kind, dsc.plane, jq, pa.jloop[jq], lo, hi);
+                    hi = min(hi, t0 + cnt) - first;
+                    lo -= first;
+                    if (pa.dwin >= 0) {
+                        sink = pa.sink - first;
+                        win = dsc.T + jq - pa.dwin - first;
                     }
-                    l_lse[nq][e] *= al[e];
-                    l_out[nq][e] *= al[e];
                 }
 #pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    o[mt][nq][0] *= al[0]; o[mt][nq][1] *= al[1];
-                    o[mt][nq][2] *= al[0]; o[mt][nq][3] *= al[1];
-                }
+                for (int sb = 0; sb < C::SB; ++sb)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int kk = 16 * sb + 8 * h;
+                        float &v = x[sb][nq][e + 2 * h];
+                        if (MOD && a.cap != 0.f)
+                            v = fmaf(-2.f * a.cap, __fdividef(1.f, 1.f + exp2f(v * f)), a.cap + off);
+                        else
+                            v = fmaf(v, f, off);
+                        if (MOD) v = fmaf(slope, dist + static_cast<float>(kk), v);
+                        if (!FAST) {
+                            bool vis = kk >= lo && kk < hi;
+                            if (pa.dwin >= 0) vis = vis && (kk < sink || kk >= win);
+                            v = vis ? v : -INFINITY;
+                        }
+                    }
             }
-        }
-        float tl[NQT][2];
+    };
+
+    // P of 16 keys as B fragments (keys x query columns); adds to the columns' sums
+    auto weigh = [&](const float (&x)[NQT][4], float (&tl)[NQT][2], float (&tr)[NQT][2], uint32_t (&pb)[NQT][2], auto half_tag) {
+        constexpr bool HALF = decltype(half_tag)::value;
 #pragma unroll
-        for (int nq = 0; nq < NQT; ++nq) tl[nq][0] = tl[nq][1] = 0.f;
-#pragma unroll
-        for (int sb = 0; sb < C::SB; ++sb) {
-            if (!act[sb]) continue;
-            const int kb = kg * C::SB + sb;
-            uint32_t pb[NQT][2];
-#pragma unroll
-            for (int nq = 0; nq < NQT; ++nq) {
-                // no reference yet: every score so far is -inf, or NaN
-                const float r0 = m_ref[nq][0] == -INFINITY ? 0.f : m_ref[nq][0];
-                const float r1 = m_ref[nq][1] == -INFINITY ? 0.f : m_ref[nq][1];
-                const float p0 = exp2f(x[sb][nq][0] - r0), p1 = exp2f(x[sb][nq][1] - r1);
-                const float p2 = exp2f(x[sb][nq][2] - r0), p3 = exp2f(x[sb][nq][3] - r1);
-                tl[nq][0] += p0 + p2;
-                tl[nq][1] += p1 + p3;
-                uint32_t lo, hi;
-                if constexpr (HALF) {
-                    const __half2 l2 = __floats2half2_rn(p0, p1), h2 = __floats2half2_rn(p2, p3);
-                    lo = *reinterpret_cast<const uint32_t *>(&l2);
-                    hi = *reinterpret_cast<const uint32_t *>(&h2);
-                } else {
-                    // bf16 rounds to 2^-9: normalise by the rounded values, which is what O sums
-                    const __nv_bfloat162 l2 = __floats2bfloat162_rn(p0, p1), h2 = __floats2bfloat162_rn(p2, p3);
-                    l_out[nq][0] += __low2float(l2) + __low2float(h2);
-                    l_out[nq][1] += __high2float(l2) + __high2float(h2);
-                    lo = *reinterpret_cast<const uint32_t *>(&l2);
-                    hi = *reinterpret_cast<const uint32_t *>(&h2);
-                }
-                pb[nq][0] = movmatrix_t(lo);
-                pb[nq][1] = movmatrix_t(hi);
-            }
+        for (int nq = 0; nq < NQT; ++nq) {
+            const float p0 = exp2f(x[nq][0]), p1 = exp2f(x[nq][1]), p2 = exp2f(x[nq][2]), p3 = exp2f(x[nq][3]);
+            tl[nq][0] += p0 + p2;
+            tl[nq][1] += p1 + p3;
+            uint32_t lo, hi;
             if constexpr (HALF) {
+                const __half2 l2 = __floats2half2_rn(p0, p1), h2 = __floats2half2_rn(p2, p3);
+                lo = *reinterpret_cast<const uint32_t *>(&l2);
+                hi = *reinterpret_cast<const uint32_t *>(&h2);
+            } else {
+                // bf16 rounds to 2^-8: the output is normalised by the rounded values, which is what O sums
+                const __nv_bfloat162 l2 = __floats2bfloat162_rn(p0, p1), h2 = __floats2bfloat162_rn(p2, p3);
+                tr[nq][0] += __low2float(l2) + __low2float(h2);
+                tr[nq][1] += __high2float(l2) + __high2float(h2);
+                lo = *reinterpret_cast<const uint32_t *>(&l2);
+                hi = *reinterpret_cast<const uint32_t *>(&h2);
+            }
+            pb[nq][0] = movmatrix_t(lo);
+            pb[nq][1] = movmatrix_t(hi);
+        }
+    };
+
+    // O^T += V^T P^T over the 16 keys of sub-block kb, for MT column tiles of head_dim from tile mt0 on
+    auto accumulate = [&](const TileDesc &dsc, uint32_t kb0, int t0, int cnt, int kb, int mt0, const uint32_t (&pb)[NQT][2],
+                          auto fast_tag, auto half_tag) {
+        constexpr bool FAST = decltype(fast_tag)::value, HALF = decltype(half_tag)::value;
+        if constexpr (HALF) {
+            const uint32_t v0 = kb0 + 64 * D + kb * 16 * D + lane * 16;
+            if constexpr (C::MT == 1) {
+                const uint2 w = lds64(v0 + (mt0 >> 1) * 512 + (mt0 & 1) * 8);
+                uint32_t af[4];
+                q8_to_f16(w.x, af[0], af[2]);
+                q8_to_f16(w.y, af[1], af[3]);
 #pragma unroll
-                for (int mp = 0; mp < D / 32; ++mp) {
-                    const uint4 w = lds128(vb0 + kb * 16 * D + (mp * 32 + lane) * 16);
+                for (int nq = 0; nq < NQT; ++nq) mma_step<true, false>(o[0][nq], af, pb[nq][0], pb[nq][1]);
+            } else {
+#pragma unroll
+                for (int mp = 0; mp < C::MT / 2; ++mp) {
+                    const uint4 w = lds128(v0 + (mt0 / 2 + mp) * 512);
                     uint32_t af[4];
                     q8_to_f16(w.x, af[0], af[2]);
                     q8_to_f16(w.y, af[1], af[3]);
 #pragma unroll
-                    for (int nq = 0; nq < NQT; ++nq) mma_16816_f16(o[2 * mp][nq], af, pb[nq][0], pb[nq][1]);
+                    for (int nq = 0; nq < NQT; ++nq) mma_step<true, false>(o[2 * mp][nq], af, pb[nq][0], pb[nq][1]);
                     q8_to_f16(w.z, af[0], af[2]);
                     q8_to_f16(w.w, af[1], af[3]);
 #pragma unroll
-                    for (int nq = 0; nq < NQT; ++nq) mma_16816_f16(o[2 * mp + 1][nq], af, pb[nq][0], pb[nq][1]);
+                    for (int nq = 0; nq < NQT; ++nq) mma_step<true, false>(o[2 * mp + 1][nq], af, pb[nq][0], pb[nq][1]);
+                }
+            }
+        } else {
+            const uint32_t v0 = kb0 + C::RING_BYTES / 2 + (static_cast<uint32_t>(16 * kb) + vrow_off) * 64;
+            auto v_frag = [&](int mt, uint32_t (&af)[4]) {
+                const uint32_t col16 = static_cast<uint32_t>(2 * (mt & 1)) + vcol_sel;
+                ldsm_x4_t(v0 + (mt >> 1) * kBox + ((col16 ^ swz) << 4), af[0], af[1], af[2], af[3]);
+            };
+            bool odd = false;  // a masked tile holding infinities or NaN (stale rows and unwritten ones included)
+            if constexpr (!FAST) {
+                for (int mt = 0; mt < C::MT; ++mt) {
+                    uint32_t af[4];
+                    v_frag(mt0 + mt, af);
+                    odd = odd || bf16x2_nonfinite(af[0]) || bf16x2_nonfinite(af[1]) || bf16x2_nonfinite(af[2]) ||
+                          bf16x2_nonfinite(af[3]);
+                }
+                odd = __any_sync(0xffffffffu, odd);
+            }
+            if (!odd) {
+#pragma unroll
+                for (int mt = 0; mt < C::MT; ++mt) {
+                    uint32_t af[4];
+                    v_frag(mt0 + mt, af);
+#pragma unroll
+                    for (int nq = 0; nq < NQT; ++nq) mma_step<false, false>(o[mt][nq], af, pb[nq][0], pb[nq][1]);
                 }
             } else {
-                const uint32_t vrow = static_cast<uint32_t>(16 * kb) + vrow_off;
-                auto v_frag = [&](int mt, uint32_t (&af)[4]) {
-                    const uint32_t col16 = static_cast<uint32_t>(2 * (mt & 1)) + vcol_sel;
-                    ldsm_x4_t(vb0 + (mt >> 1) * kBoxBytes + vrow * 64 + ((col16 ^ swz) << 4), af[0], af[1], af[2], af[3]);
-                };
-                bool odd = false;  // a masked tile holding infinities or NaN
-                if constexpr (!FAST) {
-                    for (int mt = 0; mt < D / 16; ++mt) {
-                        uint32_t af[4];
-                        v_frag(mt, af);
-                        odd = odd || bf16x2_nonfinite(af[0]) || bf16x2_nonfinite(af[1]) || bf16x2_nonfinite(af[2]) ||
-                              bf16x2_nonfinite(af[3]);
-                    }
-                    odd = __any_sync(0xffffffffu, odd);
-                }
-                if (!odd) {
-#pragma unroll
-                    for (int mt = 0; mt < D / 16; ++mt) {
-                        uint32_t af[4];
-                        v_frag(mt, af);
-#pragma unroll
-                        for (int nq = 0; nq < NQT; ++nq) mma_16816(o[mt][nq], af, pb[nq][0], pb[nq][1]);
-                    }
-                } else {
-                    // 0 * NaN would reach queries that do not see the row: one column at a time, with the
-                    // rows that it does not see taken out of V
-#pragma unroll
-                    for (int nq = 0; nq < NQT; ++nq)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t lo = __ballot_sync(0xffffffffu, x[sb][nq][e] != -INFINITY);
-                            const uint32_t hi = __ballot_sync(0xffffffffu, x[sb][nq][e + 2] != -INFINITY);
-                            for (int cc = 0; cc < 4; ++cc) {  // column 8 nq + 2 cc + e
-                                const uint32_t b0 = (lo >> (8 * c4 + cc)) & 1u, b1 = (lo >> (8 * c4 + 4 + cc)) & 1u;
-                                const uint32_t b2 = (hi >> (8 * c4 + cc)) & 1u, b3 = (hi >> (8 * c4 + 4 + cc)) & 1u;
-                                const uint32_t m01 = b0 * 0xFFFFu + b1 * 0xFFFF0000u;  // keys 2 c4, 2 c4 + 1
-                                const uint32_t m23 = b2 * 0xFFFFu + b3 * 0xFFFF0000u;  // and 8 more
-#pragma unroll
-                                for (int mt = 0; mt < D / 16; ++mt) {
-                                    uint32_t af[4];
-                                    v_frag(mt, af);
-                                    af[0] &= m01; af[1] &= m01; af[2] &= m23; af[3] &= m23;
-                                    float t4[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma_16816(t4, af, pb[nq][0], pb[nq][1]);
-                                    if (c4 == cc) {
-                                        o[mt][nq][e] += t4[e];
-                                        o[mt][nq][e + 2] += t4[e + 2];
-                                    }
-                                }
-                            }
+                // 0 * NaN would reach queries that do not see the row: one block position at a time, with
+                // the rows that it does not see taken out of V
+                for (int j = pa.j0; j < pa.j0 + a.qB; ++j) {
+                    uint32_t m01 = 0, m23 = 0;  // this thread's keys 2 c4, 2 c4 + 1, and 8 more
+#pragma unroll 1
+                    for (int u = 0; u < 4; ++u) {
+                        const int kk = 16 * kb + 2 * c4 + (u & 1) + 4 * (u & 2);
+                        if (kk < cnt && score_sees(pa, dsc.T, dsc.kind, dsc.plane, t0 + kk, j, pa.jloop[j])) {
+                            const uint32_t m = 0xFFFFu << (16 * (u & 1));
+                            m01 |= u < 2 ? m : 0u;
+                            m23 |= u < 2 ? 0u : m;
                         }
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < C::MT; ++mt) {
+                        uint32_t af[4];
+                        v_frag(mt0 + mt, af);
+                        af[0] &= m01; af[1] &= m01; af[2] &= m23; af[3] &= m23;
+#pragma unroll
+                        for (int nq = 0; nq < NQT; ++nq) {
+                            float t4[4];
+                            mma_step<false, true>(t4, af, pb[nq][0], pb[nq][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (qpos[col0 + 8 * nq + (e & 1)] == j) o[mt][nq][e] += t4[e];
+                        }
+                    }
                 }
             }
         }
+    };
+
+    // the block's sums into the columns' (8-bit: over the V scale).  0 * NaN: a column that sees none of a block
+    // that reads as NaN takes nothing from it
+    auto add_sums = [&](const float (&tl)[NQT][2], const float (&tr)[NQT][2], float iv, auto fast_tag, auto half_tag) {
+        constexpr bool FAST = decltype(fast_tag)::value, HALF = decltype(half_tag)::value;
 #pragma unroll
         for (int nq = 0; nq < NQT; ++nq)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                if constexpr (HALF) {
-                    // 0 * NaN: a column that sees none of a block that reads as NaN takes nothing from it
-                    const float s = !FAST && tl[nq][e] == 0.f ? 0.f : tl[nq][e] * iv;
-                    l_lse[nq][e] += s;
-                    l_out[nq][e] += s;
-                } else {
-                    l_lse[nq][e] += tl[nq][e];
-                }
+                const float s = !HALF ? tl[nq][e] : !FAST && tl[nq][e] == 0.f ? 0.f : tl[nq][e] * iv;
+                l_lse[nq][e] += s;
+                l_out[nq][e] += HALF ? s : tr[nq][e];
             }
     };
 
+    // moves a column's reference up by `up` (al: what its sums are worth then)
+    auto move_ref = [&](int nq, int e, float up, float al, float (&x)[C::SB][NQT][4]) {
+        m_ref[nq][e] += up;
+        l_lse[nq][e] *= al;
+        l_out[nq][e] *= al;
+#pragma unroll
+        for (int sb = 0; sb < C::SB; ++sb) {
+            x[sb][nq][e] -= up;
+            x[sb][nq][e + 2] -= up;
+        }
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) {
+            o[mt][nq][e] *= al;
+            o[mt][nq][e + 2] *= al;
+        }
+    };
+    auto column_max = [&](const float (&x)[C::SB][NQT][4], int nq, int e) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int sb = 0; sb < C::SB; ++sb) m = fmaxf(m, fmaxf(x[sb][nq][e], x[sb][nq][e + 2]));
+        return m;
+    };
+
+    // ---------------------------------------------------------------- a block, each warp on its own keys
+    auto compute = [&](const TileDesc &dsc, uint32_t kb0, int t0, int cnt, auto fast_tag, auto half_tag) {
+        constexpr bool FAST = decltype(fast_tag)::value, HALF = decltype(half_tag)::value;
+        float x[C::SB][NQT][4];
+        Scales sc = {1.f, 0.f, 1.f};
+        if constexpr (HALF) sc = scales_of(kb0);
+#pragma unroll
+        for (int sb = 0; sb < C::SB; ++sb) {
+            const int kb = kg * C::SB + sb;
+            if (!FAST && 16 * kb >= cnt) {
+#pragma unroll
+                for (int nq = 0; nq < NQT; ++nq) x[sb][nq][0] = x[sb][nq][1] = x[sb][nq][2] = x[sb][nq][3] = 0.f;
+            } else {
+                scores(kb0, kb, x[sb], half_tag);
+            }
+        }
+        relative(dsc, t0, cnt, kg * C::SB, sc, x, fast_tag, half_tag);
+        // The reference moves when a score exceeds it by more than kScoreHi, or when the column has no sum
+        // yet; the warp looks at a column's maximum over all lanes only if one lane calls for it.
+        bool over = false;
+#pragma unroll
+        for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                over = over || column_max(x, nq, e) > (l_lse[nq][e] == 0.f ? -INFINITY : kScoreHi);
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mt = column_max(x, nq, e), l = l_lse[nq][e];
+#pragma unroll
+                    for (int s = 4; s < 32; s <<= 1) {
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, s));
+                        l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, s));
+                    }
+                    if (mt > (l == 0.f ? -INFINITY : kScoreHi))
+                        move_ref(nq, e, mt - kScoreLo, l == 0.f ? 1.f : exp2f(kScoreLo - mt), x);
+                }
+        }
+        float tl[NQT][2], tr[NQT][2];
+#pragma unroll
+        for (int nq = 0; nq < NQT; ++nq) tl[nq][0] = tl[nq][1] = tr[nq][0] = tr[nq][1] = 0.f;
+#pragma unroll
+        for (int sb = 0; sb < C::SB; ++sb) {
+            const int kb = kg * C::SB + sb;
+            if (!FAST && 16 * kb >= cnt) continue;
+            uint32_t pb[NQT][2];
+            weigh(x[sb], tl, tr, pb, half_tag);
+            accumulate(dsc, kb0, t0, cnt, kb, 0, pb, fast_tag, half_tag);
+        }
+        add_sums(tl, tr, sc.iv, fast_tag, half_tag);
+    };
+
+    // ---------------------------------------------------------------- a block, by the four warps of a wide group
+    // Warp kg forms P of sub-block kg and leaves it in shared memory; then it adds all sub-blocks to its quarter
+    // of O.  All four keep the same references: a block that has to move one says so before the barrier, and
+    // is weighed again after its warps have compared their maxima.  P is double-buffered: a warp that writes the
+    // buffer of block n + 2 has passed the barrier of block n + 1, which its readers reach after block n.
+    int nblk = 0;
+    const uint32_t pbuf0 = smem_addr(qf) + C::Q_BYTES + tg * (C::P_BYTES / TG) + lane * 16;
+    auto compute_wide = [&](const TileDesc &dsc, uint32_t kb0, int t0, int cnt, auto fast_tag, auto half_tag) {
+        constexpr bool FAST = decltype(fast_tag)::value, HALF = decltype(half_tag)::value;
+        constexpr int PT = (NQT / 2) * 512;  // bytes of P of a sub-block
+        const uint32_t pbuf = pbuf0 + (nblk & 1) * 4 * PT;
+        const bool mine = FAST || 16 * kg < cnt;
+        float x[C::SB][NQT][4], tl[NQT][2], tr[NQT][2];
+        Scales sc = {1.f, 0.f, 1.f};
+        if constexpr (HALF) sc = scales_of(kb0);
+        auto put = [&]() {
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq) tl[nq][0] = tl[nq][1] = tr[nq][0] = tr[nq][1] = 0.f;
+            uint32_t pb[NQT][2];
+            weigh(x[0], tl, tr, pb, half_tag);
+#pragma unroll
+            for (int i = 0; i < NQT / 2; ++i)
+                sts128(pbuf + kg * PT + i * 512,
+                       make_uint4(pb[2 * i][0], pb[2 * i][1], pb[2 * i + 1][0], pb[2 * i + 1][1]));
+        };
+        if (mine) {
+            scores(kb0, kg, x[0], half_tag);
+            relative(dsc, t0, cnt, kg, sc, x, fast_tag, half_tag);
+            bool over = false;
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    over = over || column_max(x, nq, e) > (seen >> (2 * nq + e) & 1 ? kScoreHi : -INFINITY);
+            if (__any_sync(0xffffffffu, over) && lane == 0) gflag[4 * tg + (nblk & 1)] = nblk;
+            put();
+        } else {
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq) {
+                tl[nq][0] = tl[nq][1] = tr[nq][0] = tr[nq][1] = 0.f;
+                x[0][nq][0] = x[0][nq][1] = x[0][nq][2] = x[0][nq][3] = -INFINITY;
+            }
+        }
+        named_bar_sync(2 + tg, 128);
+        const uint4 flags = lds128(smem_addr(gflag + 4 * tg));
+        if (flags.z != ~0u) {  // a warp of the group gave up waiting for this tile
+            aborted = true;
+            return;
+        }
+        if (static_cast<int>(nblk & 1 ? flags.y : flags.x) == nblk) {
+            float *gm = gmax + tg * 4 * C::NQ;
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mt = column_max(x, nq, e);
+#pragma unroll
+                    for (int s = 4; s < 32; s <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, s));
+                    if (g4 == 0) gm[kg * C::NQ + 8 * nq + 2 * c4 + e] = mt;
+                }
+            named_bar_sync(2 + tg, 128);
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float *g = gm + 8 * nq + 2 * c4 + e;
+                    const float mt = fmaxf(fmaxf(g[0], g[C::NQ]), fmaxf(g[2 * C::NQ], g[3 * C::NQ]));
+                    const bool has = seen >> (2 * nq + e) & 1;
+                    if (mt > (has ? kScoreHi : -INFINITY)) {
+                        move_ref(nq, e, mt - kScoreLo, has ? exp2f(kScoreLo - mt) : 1.f, x);
+                        seen |= 1u << (2 * nq + e);
+                    }
+                }
+            if (mine) put();
+            named_bar_sync(2 + tg, 128);
+        }
+        if (16 * C::MT * kg < D) {
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                if (!FAST && 16 * kb >= cnt) continue;
+                uint32_t pb[NQT][2];
+#pragma unroll
+                for (int i = 0; i < NQT / 2; ++i) {
+                    const uint4 w = lds128(pbuf + kb * PT + i * 512);
+                    pb[2 * i][0] = w.x;
+                    pb[2 * i][1] = w.y;
+                    pb[2 * i + 1][0] = w.z;
+                    pb[2 * i + 1][1] = w.w;
+                }
+                accumulate(dsc, kb0, t0, cnt, kb, C::MT * kg, pb, fast_tag, half_tag);
+            }
+        }
+        add_sums(tl, tr, sc.iv, fast_tag, half_tag);
+        ++nblk;
+    };
+    auto block = [&](const TileDesc &dsc, uint32_t kb0, int t0, int cnt, auto fast_tag, auto half_tag) {
+        if constexpr (C::WIDE) compute_wide(dsc, kb0, t0, cnt, fast_tag, half_tag);
+        else compute(dsc, kb0, t0, cnt, fast_tag, half_tag);
+    };
+
     const bool ring_all_visible = pa.nloops == 1 && pa.dwin < 0;
+    int fin_next = P_first;
     reset_state();
     if (a.early) pdl_wait();  // the caller may be writing the queries
+    stage_q(P_first);
     for (int i = tg; i < ntiles; i += TG) {
         const int s = i % NS;
         if (!mbar_wait_bounded(full0 + 8 * s, (i / NS) & 1)) {
             aborted = true;
             atomicOr(a.err, RIPE_DEVERR_WAIT_TIMEOUT);
             *reinterpret_cast<volatile int *>(&sflag[1]) = 1;
+            if constexpr (C::WIDE) {  // the group's other warps may be waiting for this one's P: all four stop here
+                if (lane == 0) gflag[4 * tg + 2] = 1;
+                __syncwarp();
+                named_bar_sync(2 + tg, 128);
+            }
             break;
         }
         const TileDesc dsc = sdesc[s];
-        const bool half = Q8 && dsc.kind == kDeep;
-        if (dsc.pair != st_pair) {
-            if (st_pair >= 0 || fin_next < dsc.pair) {
-                while (fin_next < dsc.pair) {
-                    finalize(fin_next, st_pair == fin_next);
-                    ++fin_next;
-                }
-                reset_state();
-            }
-            st_pair = dsc.pair;
-            load_q(dsc.n, dsc.kh, half);
-        } else if (Q8 && half != st_half) {
-            load_q(dsc.n, dsc.kh, half);
+        while (fin_next < dsc.pair) {
+            finalize(fin_next, st_pair == fin_next);
+            ++fin_next;
         }
+        st_pair = dsc.pair;
+        const bool half = Q8 && dsc.kind == kDeep;
+        if (!C::WIDE && st_half != (half ? 1 : 0)) load_q(half);
         const uint32_t base = stage0 + s * C::STAGE_BYTES;
         // mask-free: deepest-plane rows outside a draft window, or a full ring tile that every query of
         // the call sees whole (one loop; every key before the first query and in the last one's window)
@@ -853,18 +1063,19 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                 for (int b = 0; b < (dsc.cnt >> 6); ++b) {
                     const uint32_t rb = base + b * q8_record_bytes(D);
                     if (whole)
-                        compute(dsc, rb, dsc.t0 + 64 * b, 64, std::true_type(), std::true_type());
+                        block(dsc, rb, dsc.t0 + 64 * b, 64, std::true_type(), std::true_type());
                     else
-                        compute(dsc, rb, dsc.t0 + 64 * b, 64, std::false_type(), std::true_type());
+                        block(dsc, rb, dsc.t0 + 64 * b, 64, std::false_type(), std::true_type());
                 }
             }
         }
         if (!half) {
-            if (whole && dsc.cnt == kTileRows)
-                compute(dsc, base, dsc.t0, dsc.cnt, std::true_type(), std::false_type());
+            if (!Q8 && whole && dsc.cnt == kTileRows)
+                block(dsc, base, dsc.t0, dsc.cnt, std::true_type(), std::false_type());
             else
-                compute(dsc, base, dsc.t0, dsc.cnt, std::false_type(), std::false_type());
+                block(dsc, base, dsc.t0, dsc.cnt, std::false_type(), std::false_type());
         }
+        if (C::WIDE && aborted) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(empty0 + 8 * s);
     }
@@ -902,26 +1113,24 @@ struct ScoreInst {
     }
 };
 
-// Query-side configuration by the query rows per kv head: the one that ripe_verify.cu measured best
-// for its tiles (RIPE_QCFG_LIST).
+// Query-side configuration by the query rows of a row group.
 template <int D, bool Q8, bool MOD>
 struct ScoreSet {
     using R8 = ScoreInst<D, 1, 1, 4, 2, Q8, MOD>;
     using R16 = ScoreInst<D, 2, 1, 4, 2, Q8, MOD>;
-    using R32 = ScoreInst<D, 2, 2, 2, 2, Q8, MOD>;
-    using R64 = ScoreInst<D, 2, 4, 2, 1, Q8, MOD>;
+    using Wide = ScoreInst<D, 4, 1, 4, 3, Q8, MOD>;
+    using Narrow = ScoreInst<D, 2, 2, 2, 2, Q8, MOD>;
+    using R32 = std::conditional_t<Q8, Wide, Narrow>;
     static cudaError_t set_attr() {
         cudaError_t e = R8::set_attr();
         if (e == cudaSuccess) e = R16::set_attr();
         if (e == cudaSuccess) e = R32::set_attr();
-        if (e == cudaSuccess) e = R64::set_attr();
         return e;
     }
     static cudaError_t launch(const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s) {
-        if (a.Mq <= 8) return R8::launch(t, grid, a, s);
-        if (a.Mq <= 16) return R16::launch(t, grid, a, s);
-        if (a.Mq <= 32) return R32::launch(t, grid, a, s);
-        return R64::launch(t, grid, a, s);
+        if (a.grows <= 8) return R8::launch(t, grid, a, s);
+        if (a.grows <= 16) return R16::launch(t, grid, a, s);
+        return R32::launch(t, grid, a, s);
     }
 };
 

@@ -3,7 +3,7 @@
 // tests/test_score_plan.py compiles it with nvcc; nothing here runs on a GPU.
 //
 // Input, one case per line:
-//   T W R max_T max_B mode unit B j0 qB sink window nloops loop_0 .. loop_{nloops-1}
+//   T W R max_T max_B mode unit wide B j0 qB sink window nloops loop_0 .. loop_{nloops-1}
 //     queries at block positions j0 .. j0 + qB - 1, position j at loop_{j mod nloops}
 // Output per case: "S deep_rows", one line "kind t0 cnt y plane bits_0 .. bits_{qB-1}" per tile (bit i of
 // bits_q: query q sees key t0 + i), then "E total".
@@ -22,9 +22,9 @@ int main(int argc, char **) {
                     std::printf("%d %d %d %d %d\n", d, t, e, q8_k_offset(t, e, d), q8_v_offset(t, e, d));
         return 0;
     }
-    int T, W, R, max_T, max_B, mode, unit, B, j0, qB, sink, window, nloops, loops[kMaxQueryRows];
-    while (std::scanf("%d %d %d %d %d %d %d %d %d %d %d %d %d", &T, &W, &R, &max_T, &max_B, &mode, &unit, &B, &j0, &qB,
-                      &sink, &window, &nloops) == 13) {
+    int T, W, R, max_T, max_B, mode, unit, wide, B, j0, qB, sink, window, nloops, loops[kMaxQueryRows];
+    while (std::scanf("%d %d %d %d %d %d %d %d %d %d %d %d %d %d", &T, &W, &R, &max_T, &max_B, &mode, &unit, &wide, &B, &j0, &qB,
+                      &sink, &window, &nloops) == 14) {
         for (int k = 0; k < nloops; ++k)
             if (std::scanf("%d", &loops[k]) != 1) return 2;
         // cache geometry (ripe_cache_alloc, ripe_cache_alloc_q8)
@@ -39,6 +39,8 @@ int main(int argc, char **) {
         p.unit = unit;
         p.deep_box = (deep_rows == 0 || deep_rows >= kTileRows) ? kTileRows : deep_rows;
         p.ring_box = S < kTileRows ? S : kTileRows;
+        if (wide && p.ring_box > kWideRingRows) p.ring_box = kWideRingRows;
+        p.deep_tile = unit > 1 && !wide ? 2 * kQ8Block : kTileRows;
         p.crel = mode;
         p.sink = sink;
         p.dwin = window;

@@ -43,26 +43,27 @@ def _cases():
             max_T = T + max_B + rng.choice((0, 1, 40, 300))
             mode = rng.randint(0, 1)
             kind = rng.randint(0, 3)
+            wide = rng.randint(0, 1) if unit > 1 else 0  # smaller tiles, for more than 16 query rows
             if kind < 2:  # one loop
                 B = rng.randint(1, max_B)
-                out.append((T, W, R, max_T, max_B, mode, unit, B, 0, B, 0, -1, [rng.randrange(R)]))
+                out.append((T, W, R, max_T, max_B, mode, unit, wide, B, 0, B, 0, -1, [rng.randrange(R)]))
             elif kind == 2:  # a loop per position
                 B = rng.randint(1, max_B)
-                out.append((T, W, R, max_T, max_B, mode, unit, B, 0, B, 0, -1, [rng.randrange(R) for _ in range(B)]))
+                out.append((T, W, R, max_T, max_B, mode, unit, wide, B, 0, B, 0, -1, [rng.randrange(R) for _ in range(B)]))
             else:  # a draft step
                 j = rng.randrange(max_B)
                 sink, window = rng.choice(((0, -1), (0, 0), (4, 30), (100, 10), (64, 64), (1 << 30, 5), (3, 1 << 30)))
-                out.append((T, W, R, max_T, max_B, mode, unit, j + 1, j, 1, sink, window, [rng.randrange(R)]))
+                out.append((T, W, R, max_T, max_B, mode, unit, wide, j + 1, j, 1, sink, window, [rng.randrange(R)]))
     return out
 
 
 def test_every_query_sees_its_keys_once_at_their_plane(dump_exe):
     cases = _cases()
-    text = "\n".join(" ".join(map(str, (*c[:12], len(c[12]), *c[12]))) for c in cases) + "\n"
+    text = "\n".join(" ".join(map(str, (*c[:13], len(c[13]), *c[13]))) for c in cases) + "\n"
     lines = iter(subprocess.run([dump_exe], input=text, capture_output=True, text=True, check=True,
                                 timeout=120).stdout.splitlines())
     for c in cases:
-        T, W, R, max_T, max_B, mode, unit, B, j0, qB, sink, window, loops = c
+        T, W, R, max_T, max_B, mode, unit, wide, B, j0, qB, sink, window, loops = c
         Wc = min(W, max_T)
         D = max(0, T - Wc) // unit * unit
         S, deep_rows = map(int, next(lines).split())
@@ -79,10 +80,10 @@ def test_every_query_sees_its_keys_once_at_their_plane(dump_exe):
             assert cnt >= 1 and t0 >= 0
             if kind == KDEEP:
                 assert y == t0 and t0 + cnt <= D and plane == R - 1
-                assert cnt <= (128 if unit > 1 else 64)
+                assert cnt <= (128 if unit > 1 and not wide else 64)
                 assert unit == 1 or (t0 % 64 == 0 and cnt % 64 == 0)
             else:
-                assert cnt <= 64 and t0 >= D and t0 + cnt <= (T if kind == KDUAL else T + B), c
+                assert cnt <= (32 if wide else 64) and t0 >= D and t0 + cnt <= (T if kind == KDUAL else T + B), c
                 assert 0 <= y and y + cnt <= S and y == t0 % S
             for q in range(qB):
                 for i, bit in enumerate(f[5 + q]):
