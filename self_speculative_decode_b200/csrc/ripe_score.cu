@@ -4,6 +4,7 @@
 
 namespace ripe {
 
+
 cudaError_t launch_score_bf16(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s) {
     switch (d) {
         case 64: return ScoreSet<64, false, true>::launch(t, grid, a, s);
@@ -64,6 +65,12 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     p.deep_box = c->deep_box;
     p.deep_tile = q8 && !wide ? 2 * kQ8Block : kTileRows;
     p.ring_box = wide && c->ring_box > kWideRingRows ? kWideRingRows : c->ring_box;
+    // A masked tile takes about as long as two deepest-plane tiles, and the end of a head (merging the warps' partials,
+    // the next head's queries) as long as 4, or 8 where 9 to 32 rows leave less of a tile's time to the copies.
+    // Measured on uneven batches of 32 sequences (10 .. 9000 keys; 8-bit: 4, 16 and 32 rows a kv head): 61, 70 and
+    // 58 us, against 102, 154 and 150 us with every tile at 1 and heads at 0.
+    p.ring_cost = 2;
+    p.head_cost = q8 && a.grows > 8 ? 8 : 4;
     p.crel = c->mode == RIPE_WINDOW_CACHE_RELATIVE ? 1 : 0;
     p.sink = call.sink;
     p.dwin = call.window;
@@ -97,7 +104,7 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     int grid = c->num_sms < 256 ? c->num_sms : 256;
     if (c->synced) {
         long total = 0;
-        for (int n = 0; n < c->N; ++n) total += static_cast<long>(score_geom(c->T[n], p).total) * c->kvH * a.groups;
+        for (int n = 0; n < c->N; ++n) total += static_cast<long>(score_geom(c->T[n], p).cost) * c->kvH * a.groups;
         const long need = (total + a.min_chunk - 1) / a.min_chunk;
         if (need < grid) grid = static_cast<int>(need);
     }

@@ -49,6 +49,8 @@ struct ScorePlan {
     int W, B, R, S, unit;
     int deep_box, ring_box;
     int deep_tile;    // rows of a DEEP tile: 64, or 128 (two 8-bit blocks)
+    int ring_cost;    // what a RING or DUAL tile costs, in DEEP tiles
+    int head_cost;    // what a head costs beside its tiles
     int crel;         // cache-relative window
     int all_deepest;  // a single loop, the deepest one
     int sink, dwin;   // windowed draft (dwin >= 0), as PlanArgs
@@ -67,7 +69,13 @@ struct ScoreGeom {
     int e1, b2, nd1, nd;  // DEEP rows [0, e1) in nd1 tiles, then [b2, D)
     ScoreSeg ring, dual;
     int total;
+    int cost;  // of the whole list, in DEEP tiles
 };
+
+// tiles of a box of 32 or 64 rows (ring) by shifts
+__host__ __device__ __forceinline__ int score_tiles(int rows, int box) {
+    return box == 64 ? (rows + 63) >> 6 : box == 32 ? (rows + 31) >> 5 : cdiv(rows, box);
+}
 
 __host__ __device__ __forceinline__ ScoreSeg score_seg(int p0, int len, const ScorePlan &a) {
     ScoreSeg s;
@@ -75,8 +83,8 @@ __host__ __device__ __forceinline__ ScoreSeg score_seg(int p0, int len, const Sc
     s.len = len > 0 ? len : 0;
     s.slot0 = p0 % a.S;
     s.first = s.len < a.S - s.slot0 ? s.len : a.S - s.slot0;
-    s.n1 = ctiles(s.first, a.ring_box);
-    s.n = s.n1 + ctiles(s.len - s.first, a.ring_box);
+    s.n1 = score_tiles(s.first, a.ring_box);
+    s.n = s.n1 + score_tiles(s.len - s.first, a.ring_box);
     return s;
 }
 
@@ -94,8 +102,8 @@ __host__ __device__ __forceinline__ ScoreGeom score_geom(int T, const ScorePlan 
         ws = ws < 0 ? 0 : ws > s.D ? s.D : ws;
         s.b2 = (ws & ~63) > s.e1 ? ws & ~63 : s.e1;
     }
-    s.nd1 = cdiv(s.e1, tr);
-    s.nd = s.nd1 + cdiv(s.D - s.b2, tr);
+    s.nd1 = tr == 64 ? (s.e1 + 63) >> 6 : (s.e1 + 127) >> 7;
+    s.nd = s.nd1 + (tr == 64 ? (s.D - s.b2 + 63) >> 6 : (s.D - s.b2 + 127) >> 7);
     if (a.all_deepest) {
         s.ring = score_seg(s.D, T + a.B - s.D, a);
         s.dual = score_seg(s.D, 0, a);
@@ -107,8 +115,22 @@ __host__ __device__ __forceinline__ ScoreGeom score_geom(int T, const ScorePlan 
         s.ring = score_seg(lo, T + a.B - lo, a);
         s.dual = score_seg(s.D, hi - s.D, a);
     }
-    s.total = s.nd + a.nloops * s.ring.n + s.dual.n;
+    const int masked = a.nloops * s.ring.n + s.dual.n;
+    s.total = s.nd + masked;
+    s.cost = s.nd + a.ring_cost * masked + a.head_cost;
     return s;
+}
+
+// The lists of all heads are laid end to end on a line of costs and cut into equal chunks; a tile belongs to the
+// chunk in which it begins.  score_begin: where tile lt of a head begins; score_first: the first tile of a head that
+// begins at or behind offset c (total: none).
+__host__ __device__ __forceinline__ int score_begin(const ScoreGeom &s, int lt, const ScorePlan &a) {
+    return lt < s.nd ? lt : s.nd + a.ring_cost * (lt - s.nd);
+}
+__host__ __device__ __forceinline__ int score_first(const ScoreGeom &s, int c, const ScorePlan &a) {
+    if (c <= s.nd) return c < 0 ? 0 : c;
+    const int lt = s.nd + (c - s.nd + a.ring_cost - 1) / a.ring_cost;
+    return lt < s.total ? lt : s.total;
 }
 
 __host__ __device__ __forceinline__ Tile score_tile(const ScoreGeom &s, int lt, const ScorePlan &a) {

@@ -87,16 +87,16 @@ struct SCfg {
     static_assert(MLF % 4 == 0 && (ROWS * NPF) % 4 == 0, "alignment");
     static constexpr int MISC = 1024 + 1024;
     static constexpr int AVAIL =
-        kSmemLimit - MISC - Q_BYTES - P_BYTES - 4 * (MERGE_FLOATS + MLF) - 4 * (2 * kMaxBatch + 2);
+        kSmemLimit - MISC - Q_BYTES - P_BYTES - 4 * (MERGE_FLOATS + MLF) - 4 * (3 * kMaxBatch + 2);
     static constexpr int NS_RAW = AVAIL / STAGE_BYTES > 8 ? 8 : AVAIL / STAGE_BYTES;
     static constexpr int NS = NS_RAW - NS_RAW % TG;  // a stage always serves the same tile group
     static_assert(NS >= 2, "not enough shared memory for the pipeline");
     static constexpr int SMEM_FIXED = MISC + Q_BYTES + P_BYTES + NS * STAGE_BYTES + 4 * (MERGE_FLOATS + MLF);
-    static_assert(SMEM_FIXED + 4 * (2 * kMaxBatch + 2) <= kSmemLimit, "shared memory");
+    static_assert(SMEM_FIXED + 4 * (3 * kMaxBatch + 2) <= kSmemLimit, "shared memory");
     static constexpr int MAX_PARTS =
         (NS * STAGE_BYTES) / (2 * ROWS * 4) < 256 ? (NS * STAGE_BYTES) / (2 * ROWS * 4) : 256;
     static_assert(MAX_PARTS >= 148, "stage buffers too small for the end-of-CTA merge");
-    static constexpr int smem_bytes(int N) { return SMEM_FIXED + (2 * N + 2) * 4; }
+    static constexpr int smem_bytes(int N) { return SMEM_FIXED + (3 * N + 2) * 4; }
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -104,6 +104,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                  : "memory");
 }
+
+__device__ __forceinline__ void l2_prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -161,60 +163,153 @@ __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t r) {
     return (r & 0x7F80u) == 0x7F80u || (r & 0x7F800000u) == 0x7F800000u;
 }
 
-// The chunk of the concatenated tile lists that this CTA streams (as plan_chunks in ripe_verify.cuh).
+// The chunk of the heads' tile lists that this CTA streams (score_begin, score_first): from tile lt of pair p_first on,
+// ntiles tiles, the last of them in pair p_last.  cum[n] is where sequence n's heads begin on the line of costs,
+// real[n] the number of tiles before them.
 struct ScoreChunk {
-    int total, chunk, pieces, tot_head, head, g_begin, g_end;
+    int chunk, pieces;  // costs; pieces > 0: every head is cut into that many pieces of its own
+    int p_first, lt, p_last, ntiles;
 };
 
-__device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum, int *Ts, int *sflag, int tid, int warp,
-                                                   int lane) {
+// Tiles that begin before offset g of the line (with `upto`: at or before it); the pair of the tile that comes next
+// (upto: of the last of them), and its index.
+__device__ __forceinline__ int score_tiles_before(const ScoreArgs &a, const int *cum, const int *real, const int *Ts, int kvH,
+                                                  int g, bool upto, int &pair, int &lt) {
+    const int n = seq_of(cum, a.N, g);
+    const ScoreGeom sg = score_geom(Ts[n], a.plan);
+    const int kh = (g - cum[n]) / sg.cost, off = g - cum[n] - kh * sg.cost;
+    lt = score_first(sg, off + (upto ? 1 : 0), a.plan);
+    const int before = real[n] + kh * sg.total + lt;
+    pair = n * kvH + kh;
+    if (upto) {
+        if (--lt < 0) --pair;  // the last tile is the previous head's
+    } else if (lt == sg.total) {
+        lt = 0;  // the rest of the head's cost holds no tile; kh + 1 == kvH is the next sequence's first head
+        ++pair;
+    }
+    return before;
+}
+
+// The CTAs that hold tiles of a pair: the first of them, and how many.
+__device__ __forceinline__ int2 score_parts(const ScoreArgs &a, const ScoreChunk &c, const int *cum, const int *Ts, int kvH,
+                                            int p) {
+    const int n = p / kvH;
+    const ScoreGeom sg = score_geom(Ts[n], a.plan);
+    const int last = score_begin(sg, sg.total - 1, a.plan);
+    if (c.pieces) return make_int2(p * c.pieces, last / c.chunk + 1);
+    const int start = cum[n] + (p - n * kvH) * sg.cost, first = start / c.chunk;
+    return make_int2(first, (start + last) / c.chunk - first + 1);
+}
+
+// Chunks of `chunk` costs, or, where all heads cost the same (cost0) and there are fewer heads than CTAs, `pieces`
+// equal pieces of every head.  A head that a CTA shares costs it head_cost once more, so that pieces, which share
+// nothing across heads, are taken when they are no longer than a chunk (their own head_cost left out), and chunks
+// end on heads when that lengthens them by at most head_cost.
+__device__ __forceinline__ void score_cut(const ScoreArgs &a, int total, int cost0, bool same, int kvH, int &chunk,
+                                          int &pieces) {
+    const int grid = static_cast<int>(gridDim.x), head = a.plan.head_cost;
+    chunk = max(cdiv(total, grid), a.min_chunk);
+    pieces = 0;
+    if (!same) return;
+    if (chunk < cost0) {
+        const int P = min(grid / (a.N * kvH), cost0 / a.min_chunk);
+        if (P < 1) return;
+        const int piece = max(cdiv(cost0 - head, P), a.plan.ring_cost);  // no shorter than a tile: each holds one
+        if (piece <= chunk) {
+            chunk = piece;
+            pieces = P;
+        }
+    } else {
+        const int whole = cdiv(chunk, cost0) * cost0;
+        if (whole <= chunk + head) chunk = whole;
+    }
+}
+
+__device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum, int *real, int *Ts, int *sflag, int tid,
+                                                   int warp, int lane) {
     const int N = a.N, kvH = a.kvH * a.groups;
     ScoreChunk c;
-    for (int n = tid; n < N; n += blockDim.x) {
-        const int T = a.T[n];
-        Ts[n] = T;
-        cum[n + 1] = score_geom(T, a.plan).total * kvH;
-    }
-    if (tid == 0) cum[0] = 0;
-    __syncthreads();
-    pdl_trigger();  // the next kernel may be scheduled; it waits for this one to finish
-    if (warp == 0) {
-        int carry = 0;
-        bool same = true;
-        const int first = cum[1];
-        for (int b = 0; b < N; b += 32) {
-            const int own = (b + lane < N) ? cum[b + lane + 1] : 0;
-            same = same && __all_sync(0xffffffffu, b + lane >= N || own == first);
-            int v = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            if (b + lane < N) cum[b + lane + 1] = v + carry;
-            carry += __shfl_sync(0xffffffffu, v, 31);
+    c.ntiles = 0;
+    if (N == 1) {  // one sequence: every thread reads its length and cuts the list itself
+        const int T = a.T[0];
+        const ScoreGeom sg = score_geom(T, a.plan);
+        if (tid == 0) {
+            Ts[0] = T;
+            cum[0] = 0;
+            cum[1] = sg.cost * kvH;
+            real[0] = 0;
         }
-        if (lane == 0) {
-            int ch, pc;
-            choose_chunk(carry, first / kvH, same, static_cast<int>(gridDim.x), N, kvH, a.min_chunk, ch, pc);
-            sflag[6] = ch;
-            sflag[7] = pc;
+        score_cut(a, sg.cost * kvH, sg.cost, true, kvH, c.chunk, c.pieces);
+        __syncthreads();
+        pdl_trigger();  // the next kernel may be scheduled; it waits for this one to finish
+        if (c.pieces) {
+            c.p_first = c.p_last = blockIdx.x / c.pieces;
+            if (c.p_first >= kvH) return c;
+            const int at = (blockIdx.x - c.p_first * c.pieces) * c.chunk;
+            c.lt = score_first(sg, at, a.plan);
+            c.ntiles = score_first(sg, at + c.chunk, a.plan) - c.lt;
+            return c;
         }
-    }
-    __syncthreads();
-    c.total = cum[N];
-    c.chunk = sflag[6];
-    c.pieces = sflag[7];
-    c.tot_head = c.pieces ? cum[1] / kvH : 0;
-    c.head = 0;
-    if (c.pieces) {
-        c.head = blockIdx.x / c.pieces;
-        c.g_begin = c.head * c.tot_head + (blockIdx.x - c.head * c.pieces) * c.chunk;
-        c.g_end = min(min(c.g_begin + c.chunk, (c.head + 1) * c.tot_head), c.total);
     } else {
-        c.g_begin = blockIdx.x * c.chunk;
-        c.g_end = min(c.total, c.g_begin + c.chunk);
+        for (int n = tid; n < N; n += blockDim.x) {
+            const int T = a.T[n];
+            const ScoreGeom sg = score_geom(T, a.plan);
+            Ts[n] = T;
+            cum[n + 1] = sg.cost * kvH;
+            real[n] = sg.total * kvH;
+        }
+        if (tid == 0) cum[0] = 0;
+        __syncthreads();
+        pdl_trigger();
+        if (warp == 0) {
+            int carry = 0, rcarry = 0;
+            bool same = true;
+            const int first = cum[1];
+            for (int b = 0; b < N; b += 32) {
+                const int own = (b + lane < N) ? cum[b + lane + 1] : 0;
+                const int rown = (b + lane < N) ? real[b + lane] : 0;
+                same = same && __all_sync(0xffffffffu, b + lane >= N || own == first);
+                int v = own, r = rown;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, v, o), w = __shfl_up_sync(0xffffffffu, r, o);
+                    if (lane >= o) {
+                        v += u;
+                        r += w;
+                    }
+                }
+                if (b + lane < N) {
+                    cum[b + lane + 1] = v + carry;
+                    real[b + lane] = r + rcarry - rown;
+                }
+                carry += __shfl_sync(0xffffffffu, v, 31);
+                rcarry += __shfl_sync(0xffffffffu, r, 31);
+            }
+            if (lane == 0) {
+                int ch, pc;
+                score_cut(a, carry, first / kvH, same, kvH, ch, pc);
+                sflag[6] = ch;
+                sflag[7] = pc;
+            }
+        }
+        __syncthreads();
+        c.chunk = sflag[6];
+        c.pieces = sflag[7];
+        if (c.pieces) {
+            c.p_first = c.p_last = blockIdx.x / c.pieces;
+            if (c.p_first >= N * kvH) return c;
+            const ScoreGeom sg = score_geom(Ts[c.p_first / kvH], a.plan);
+            const int at = (blockIdx.x - c.p_first * c.pieces) * c.chunk;
+            c.lt = score_first(sg, at, a.plan);
+            c.ntiles = score_first(sg, at + c.chunk, a.plan) - c.lt;
+            return c;
+        }
     }
+    const int begin = blockIdx.x * c.chunk, end = min(cum[N], begin + c.chunk);
+    if (begin >= end) return c;
+    int lt_end;
+    const int before = score_tiles_before(a, cum, real, Ts, kvH, begin, false, c.p_first, c.lt);
+    c.ntiles = score_tiles_before(a, cum, real, Ts, kvH, end - 1, true, c.p_last, lt_end) - before;
     return c;
 }
 
@@ -244,6 +339,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     int *sflag = reinterpret_cast<int *>(sdesc + NS);                     // [16]
     int *cum = sflag + 16;                                                // [N + 1]
     int *Ts = cum + a.N + 1;                                              // [N]
+    int *real = Ts + a.N;                                                 // [N]
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -270,16 +366,12 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     }
     if (C::WIDE && tid < 4 * TG) gflag[tid] = -1;
     if (!a.early) pdl_wait();
-    const ScoreChunk cp = score_chunks(a, cum, Ts, sflag, tid, warp, lane);
-    const int chunk = cp.chunk, pieces = cp.pieces;
-    const int g_begin = cp.g_begin, g_end = cp.g_end;
-    if (g_begin >= g_end) {
+    const ScoreChunk cp = score_chunks(a, cum, real, Ts, sflag, tid, warp, lane);
+    const int ntiles = cp.ntiles, P_first = cp.p_first, P_last = cp.p_last;
+    if (ntiles <= 0) {
         if (a.early) pdl_wait();  // the launch completes only after its predecessor
         return;
     }
-    const int ntiles = g_end - g_begin;
-    const int P_first = pieces ? cp.head : pair_of(cum, N, kvH, g_begin);
-    const int P_last = pieces ? cp.head : pair_of(cum, N, kvH, g_end - 1);
     const uint32_t full0 = smem_addr(&bars[0]);
     const uint32_t empty0 = smem_addr(&bars[NS]);
     const uint32_t stage0 = smem_addr(stages);
@@ -290,7 +382,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         if (warp != C::NCW || lane != 0) return;
         int n = P_first / kvH, kh = P_first - (P_first / kvH) * kvH;
         ScoreGeom sg = score_geom(Ts[n], pa);
-        int lt = g_begin - (cum[n] + kh * sg.total);
+        int lt = cp.lt;
         bool waited = !a.early;
         int i = 0;
         for (; i < ntiles; ++i) {
@@ -337,6 +429,15 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                     kh = 0;
                     if (++n < N) sg = score_geom(Ts[n], pa);
                 }
+                if (i + 1 < ntiles) {  // bring the next pair's queries into L2
+                    const int h = kh / a.groups, row0 = kh % a.groups * a.grows, rows = min(a.grows, a.Mq - row0);
+                    for (int x = 0; x < rows; ++x) {
+                        const int j = (row0 + x) / a.g, hg = row0 + x - j * a.g;
+                        const char *qp = reinterpret_cast<const char *>(
+                            a.q + ((static_cast<size_t>(n) * a.qB + j) * a.Hq + h * a.g + hg) * D);
+                        for (int u = 0; u < 2 * D; u += 128) l2_prefetch(qp + u);
+                    }
+                }
             }
         }
         if (i < ntiles) {
@@ -368,13 +469,12 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     const uint32_t qf0 = smem_addr(qf) + NQT * rg * (D / 32) * 512 + lane * 16;
 
     float o[C::MT][NQT][4];
-    // l_lse sums the probabilities in fp32, l_out as the P V product of a bf16 tile sees them (rounded);
-    // a column's reference means nothing until some lane's l_lse is not zero
-    float m_ref[NQT][2], l_lse[NQT][2], l_out[NQT][2];
+    // l_lse sums the probabilities in fp32; l_fix sums what rounding adds to them in bf16 tiles, where the P V
+    // product sees 2^-8: the output is normalised by both together, which is what O sums.  A column's reference means nothing until some lane's l_lse is not zero
+    float m_ref[NQT][2], l_lse[NQT][2], l_fix[NQT][2];
     uint32_t seen = 0;  // WIDE: bit 2 nq + e is set once the column has a reference
     uint32_t qb[C::WIDE ? 1 : D / 16][C::WIDE ? 1 : NQT][2];  // Q as B fragments
 
-    int st_pair = P_first;
     int st_half = -1;  // qb holds the f16 (1) or bf16 (0) form
     bool aborted = false;
 
@@ -388,7 +488,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         for (int nq = 0; nq < NQT; ++nq) {
             m_ref[nq][0] = m_ref[nq][1] = 0.f;
             l_lse[nq][0] = l_lse[nq][1] = 0.f;
-            l_out[nq][0] = l_out[nq][1] = 0.f;
+            l_fix[nq][0] = l_fix[nq][1] = 0.f;
         }
     };
 
@@ -399,24 +499,39 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
 
     // All consumer warps: Q of pair p into shared memory, in fragment order.  bf16: of each 16 columns, lane
     // (g4, c4) has 2 c4, 2 c4 + 1 and 8 more; f16: 4 c4 .. 4 c4 + 3, the order of the 8-bit K fragments.
-    auto stage_q = [&](int p) {
-        for (int i = warp; i < C::ROWS; i += C::NCW) {
-            uint32_t w[(D + 63) / 64];
-            const int h = head_of(p), row = group_row(p) + i;
-            const bool have = i < rows_of(p);
-            const int j = have ? row / a.g : 0, hg = have ? row - j * a.g : 0;
+    // fetch_q starts the loads (a warp has rows warp, warp + NCW, ..; all of them in flight together), stage_q
+    // writes the rows.
+    constexpr int QW = (D + 63) / 64, QR = (C::ROWS + C::NCW - 1) / C::NCW;
+    uint32_t qw[QR][QW];
+    auto fetch_q = [&](int p) {
+        const int h = head_of(p), row0 = group_row(p), mq = rows_of(p);
+#pragma unroll
+        for (int r = 0; r < QR; ++r) {
+            const int i = warp + r * C::NCW;
+            const bool have = i < mq;
+            const int row = row0 + i, j = have ? row / a.g : 0, hg = have ? row - j * a.g : 0;
             const uint32_t *qp = reinterpret_cast<const uint32_t *>(
                 a.q + ((static_cast<size_t>(p / kvH) * a.qB + j) * a.Hq + h * a.g + hg) * D);
-            if (lane == 0) qpos[i] = have ? pa.j0 + j : -1;
-            uint32_t most = 0;  // largest magnitude of the row, as bf16 bits
 #pragma unroll
-            for (int u = 0; u < (D + 63) / 64; ++u) {
-                const bool in = have && u * 32 + lane < D / 2;
-                w[u] = in ? __ldg(qp + u * 32 + lane) : 0u;
-                most = max(most, max(w[u] & 0x7FFFu, (w[u] >> 16) & 0x7FFFu));
-            }
+            for (int u = 0; u < QW; ++u) qw[r][u] = have && u * 32 + lane < D / 2 ? __ldg(qp + u * 32 + lane) : 0u;
+        }
+    };
+    auto stage_q = [&](int p) {
+        const int h = head_of(p), row0 = group_row(p), mq = rows_of(p);
+#pragma unroll
+        for (int r = 0; r < QR; ++r) {
+            const int i = warp + r * C::NCW;
+            if (i >= C::ROWS) break;
+            const bool have = i < mq;
+            const int row = row0 + i, j = have ? row / a.g : 0, hg = have ? row - j * a.g : 0;
+            if (lane == 0) qpos[i] = have ? pa.j0 + j : -1;
+            if (MOD && lane == 0)
+                qslope[i] = a.slopes && have ? __ldg(a.slopes + h * a.g + hg) * 1.4426950408889634f : 0.f;
             float up = 1.f;
             if constexpr (Q8) {
+                uint32_t most = 0;  // largest magnitude of the row, as bf16 bits
+#pragma unroll
+                for (int u = 0; u < QW; ++u) most = max(most, max(qw[r][u] & 0x7FFFu, (qw[r][u] >> 16) & 0x7FFFu));
                 most = __reduce_max_sync(0xffffffffu, most);
                 // 2^k that brings the row's largest element into [16, 32); 1 for a row with infinities or NaN
                 const int ex = static_cast<int>(most >> 7);
@@ -424,39 +539,45 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                 up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
                 if (lane == 0) qscale[i] = a.sx * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
             }
-            if (MOD && lane == 0)
-                qslope[i] = a.slopes && have ? __ldg(a.slopes + h * a.g + hg) * 1.4426950408889634f : 0.f;
             uint8_t *dst = qf + (i >> 3) * (D / 32) * 512 + (i & 7) * 64;
 #pragma unroll
-            for (int u = 0; u < (D + 63) / 64; ++u) {
+            for (int u = 0; u < QW; ++u) {
                 const int at = u * 32 + lane, ks = at >> 3, x = at & 7;  // columns 2 at, 2 at + 1
                 if (at < D / 2) {
                     uint8_t *f = dst + (ks >> 1) * 512 + (ks & 1) * 8;
-                    *reinterpret_cast<uint32_t *>(f + (x & 3) * 16 + (x >> 2) * 4) = w[u];
+                    *reinterpret_cast<uint32_t *>(f + (x & 3) * 16 + (x >> 2) * 4) = qw[r][u];
                     if constexpr (Q8) {
-                        const __half2 h = __floats2half2_rn(__uint_as_float(w[u] << 16) * up,
-                                                            __uint_as_float(w[u] & 0xFFFF0000u) * up);
+                        const __half2 hq = __floats2half2_rn(__uint_as_float(qw[r][u] << 16) * up,
+                                                             __uint_as_float(qw[r][u] & 0xFFFF0000u) * up);
                         *reinterpret_cast<uint32_t *>(f + C::QF_BYTES + (x >> 1) * 16 + (x & 1) * 4) =
-                            *reinterpret_cast<const uint32_t *>(&h);
+                            *reinterpret_cast<const uint32_t *>(&hq);
                     }
                 }
             }
         }
         st_half = -1;
         named_bar_sync(1, nct);
+        if constexpr (C::WIDE) {  // columns without a row need no reference
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (qpos[col0 + 8 * nq + e] < 0) seen |= 1u << (2 * nq + e);
+        }
     };
 
-    // the CTAs holding tiles of pair p: c_first .. c_first + nparts - 1 (returns nparts)
-    auto parts_of = [&](int p, int &c_first) -> int {
-        const int n = p / kvH, kh = p - (p / kvH) * kvH;
-        const int tot_n = (cum[n + 1] - cum[n]) / kvH;
-        if (pieces) {
-            c_first = p * pieces;
-            return cdiv(tot_n, chunk);
-        }
-        const int start = cum[n] + kh * tot_n;
-        c_first = start / chunk;
-        return (start + tot_n - 1) / chunk - c_first + 1;
+    // The CTAs holding tiles of pair p (x: the first of them, y: how many).  Only this CTA's first and last pair can be
+    // shared; one thread has looked them up.
+    if (tid == 32) {
+        const int2 f = score_parts(a, cp, cum, Ts, kvH, P_first), l = score_parts(a, cp, cum, Ts, kvH, P_last);
+        sflag[8] = f.x;
+        sflag[9] = f.y;
+        sflag[10] = l.x;
+        sflag[11] = l.y;
+    }
+    auto parts_of = [&](int p) -> int2 {
+        return p == P_first ? make_int2(sflag[8], sflag[9]) : p == P_last ? make_int2(sflag[10], sflag[11])
+                                                                          : make_int2(static_cast<int>(blockIdx.x), 1);
     };
 
     // four columns of the output of row i (block position, head) of pair p, and its log-sum-exp
@@ -470,11 +591,26 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         if (c0 == 0 && a.lse) a.lse[orow] = (m + __log2f(ll)) * 0.69314718055994531f;
     };
 
+    // Publish this CTA's partial of the pair that tid 0 remembers (finalize's barrier and one fence cover every
+    // thread's writes); the last CTA to arrive merges the pair at its end.  Called a tile after the partial was
+    // written, when the fence no longer has to wait for the writes, and after the last tile.
+    int pending = -1;
+    auto publish = [&]() {
+        if (tid == 0 && pending >= 0) {
+            __threadfence();
+            if (arrive_last(&a.counters[pending], parts_of(pending).y, 0)) {
+                __threadfence();
+                sflag[4 + sflag[3]] = pending;
+                sflag[3] += 1;
+            }
+            pending = -1;
+        }
+    };
+
     // ---------------------------------------------------------------- finalize one pair
-    // Every consumer warp, for every pair of the CTA in order; then Q of the next pair is staged.
-    auto finalize = [&](int p, bool have) {
+    auto finalize = [&](int p) {
         const int slot = (tg * WK + kg) * WR + rg;  // this warp's (m, l)
-        if (!have) reset_state();
+        publish();  // of an earlier pair, if no tile followed it
         if (!C::WIDE || 16 * C::MT * kg < D) {
             float *mw = mo + (C::WIDE ? tg : slot) * C::NQ * C::DP + (C::WIDE ? 16 * C::MT * kg : 0);
 #pragma unroll
@@ -492,7 +628,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         for (int nq = 0; nq < NQT; ++nq)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float l = l_lse[nq][e], lb = l_out[nq][e];
+                float l = l_lse[nq][e], lb = l_fix[nq][e];
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) {
                     l += __shfl_xor_sync(0xffffffffu, l, x);
@@ -501,13 +637,11 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                 const bool none = C::WIDE ? !(seen >> (2 * nq + e) & 1) : l == 0.f;  // (the same for a wide group)
                 if (g4 == 0)
                     *reinterpret_cast<float4 *>(&mml[(slot * C::NQ + 8 * nq + 2 * c4 + e) * 4]) =
-                        make_float4(none ? -INFINITY : m_ref[nq][e], lb, l, 0.f);
+                        make_float4(none ? -INFINITY : m_ref[nq][e], l + lb, l, 0.f);
             }
         named_bar_sync(1, nct);
         const bool abort_now = *reinterpret_cast<volatile int *>(&sflag[1]) != 0;
-        int c_first;
-        const int nparts = parts_of(p, c_first);
-        const bool sole = nparts == 1;
+        const bool sole = parts_of(p).y == 1;
         for (int i = tid; i < C::ROWS; i += nct) {
             const int rgi = i / C::NQ, q = i - rgi * C::NQ;
             float M = -INFINITY;
@@ -553,26 +687,13 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             }
         }
         named_bar_sync(1, nct);  // partials written; the merge buffer is free again
-        if (!sole && !abort_now && tid == 0) {
-            // publish this CTA's partial (bar.sync + one fence covers every thread's writes)
-            __threadfence();
-            if (arrive_last(&a.counters[p], nparts, 0)) {
-                __threadfence();
-                sflag[4 + sflag[3]] = p;  // merged at the end of this CTA's tiles
-                sflag[3] += 1;
-            }
-        }
-        if (p < P_last) {
-            stage_q(p + 1);
-            reset_state();
-        }
+        if (!sole && !abort_now && tid == 0) pending = p;
     };
 
     // ---------------------------------------------------------------- merge the partials of one pair
     // Runs in the CTA that arrived last, after all of its own tiles (the stage buffers are free).
     auto merge_pair = [&](int p) {
-        int c_first;
-        const int nparts = parts_of(p, c_first), mq = rows_of(p);
+        const int c_first = parts_of(p).x, nparts = parts_of(p).y, mq = rows_of(p);
         float *pw = reinterpret_cast<float *>(stages);  // [nparts][ROWS] m, then weights
         float *pl = pw + nparts * C::ROWS;              // [nparts][ROWS] l
         for (int e = tid; e < nparts * mq; e += nct) {
@@ -681,12 +802,14 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                         auto fast_tag, auto half_tag) {
         constexpr bool FAST = decltype(fast_tag)::value, HALF = decltype(half_tag)::value;
 #pragma unroll
-        for (int nq = 0; nq < NQT; ++nq)
+        for (int nq = 0; nq < NQT; ++nq) {
+            float2 qs = make_float2(0.f, 0.f);
+            if (HALF) qs = *reinterpret_cast<const float2 *>(&qscale[col0 + 8 * nq]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int col = col0 + 8 * nq + e;
                 const int jq = FAST && !MOD ? 0 : qpos[col];
-                const float f = HALF ? sc.ks * qscale[col] : a.sx;
+                const float f = HALF ? sc.ks * (e ? qs.y : qs.x) : a.sx;
                 const float off = HALF ? sc.lv - m_ref[nq][e] : -m_ref[nq][e];
                 // distance of this lane's first key from the query (exact below 2^24), and its visible range
                 const int first = t0 + 16 * kb1 + g4;
@@ -720,6 +843,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                         }
                     }
             }
+        }
     };
 
     // P of 16 keys as B fragments (keys x query columns); adds to the columns' sums
@@ -736,7 +860,6 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                 lo = *reinterpret_cast<const uint32_t *>(&l2);
                 hi = *reinterpret_cast<const uint32_t *>(&h2);
             } else {
-                // bf16 rounds to 2^-8: the output is normalised by the rounded values, which is what O sums
                 const __nv_bfloat162 l2 = __floats2bfloat162_rn(p0, p1), h2 = __floats2bfloat162_rn(p2, p3);
                 tr[nq][0] += __low2float(l2) + __low2float(h2);
                 tr[nq][1] += __high2float(l2) + __high2float(h2);
@@ -843,7 +966,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             for (int e = 0; e < 2; ++e) {
                 const float s = !HALF ? tl[nq][e] : !FAST && tl[nq][e] == 0.f ? 0.f : tl[nq][e] * iv;
                 l_lse[nq][e] += s;
-                l_out[nq][e] += HALF ? s : tr[nq][e];
+                if (!HALF) l_fix[nq][e] += tr[nq][e] - tl[nq][e];
             }
     };
 
@@ -851,7 +974,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     auto move_ref = [&](int nq, int e, float up, float al, float (&x)[C::SB][NQT][4]) {
         m_ref[nq][e] += up;
         l_lse[nq][e] *= al;
-        l_out[nq][e] *= al;
+        l_fix[nq][e] *= al;
 #pragma unroll
         for (int sb = 0; sb < C::SB; ++sb) {
             x[sb][nq][e] -= up;
@@ -952,12 +1075,11 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         if (mine) {
             scores(kb0, kg, x[0], half_tag);
             relative(dsc, t0, cnt, kg, sc, x, fast_tag, half_tag);
-            bool over = false;
+            // (while some column has no reference yet, any score calls for the others' look)
+            float most = -INFINITY;
 #pragma unroll
-            for (int nq = 0; nq < NQT; ++nq)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    over = over || column_max(x, nq, e) > (seen >> (2 * nq + e) & 1 ? kScoreHi : -INFINITY);
+            for (int nq = 0; nq < NQT; ++nq) most = fmaxf(most, fmaxf(column_max(x, nq, 0), column_max(x, nq, 1)));
+            const bool over = most > (seen == (1u << (2 * NQT)) - 1 ? kScoreHi : -INFINITY);
             if (__any_sync(0xffffffffu, over) && lane == 0) gflag[4 * tg + (nblk & 1)] = nblk;
             put();
         } else {
@@ -1024,65 +1146,76 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         else compute(dsc, kb0, t0, cnt, fast_tag, half_tag);
     };
 
+    // Every consumer warp takes the CTA's pairs in order (finalize and stage_q synchronise all of them) and its
+    // group's tiles, each in its pair.
     const bool ring_all_visible = pa.nloops == 1 && pa.dwin < 0;
-    int fin_next = P_first;
-    reset_state();
+    int i = tg;
+    bool here = false;  // tile i has landed
     if (a.early) pdl_wait();  // the caller may be writing the queries
-    stage_q(P_first);
-    for (int i = tg; i < ntiles; i += TG) {
-        const int s = i % NS;
-        if (!mbar_wait_bounded(full0 + 8 * s, (i / NS) & 1)) {
-            aborted = true;
-            atomicOr(a.err, RIPE_DEVERR_WAIT_TIMEOUT);
-            *reinterpret_cast<volatile int *>(&sflag[1]) = 1;
-            if constexpr (C::WIDE) {  // the group's other warps may be waiting for this one's P: all four stop here
-                if (lane == 0) gflag[4 * tg + 2] = 1;
-                __syncwarp();
-                named_bar_sync(2 + tg, 128);
+    fetch_q(P_first);
+    for (int p = P_first; p <= P_last; ++p) {
+        reset_state();
+        stage_q(p);
+        while (i < ntiles) {
+            const int s = i % NS;
+            if (!here) {
+                if (!mbar_wait_bounded(full0 + 8 * s, (i / NS) & 1)) {
+                    aborted = true;
+                    atomicOr(a.err, RIPE_DEVERR_WAIT_TIMEOUT);
+                    *reinterpret_cast<volatile int *>(&sflag[1]) = 1;
+                    if constexpr (C::WIDE) {  // the group's other warps may be waiting for this one's P: all stop here
+                        if (lane == 0) gflag[4 * tg + 2] = 1;
+                        __syncwarp();
+                        named_bar_sync(2 + tg, 128);
+                    }
+                    i = ntiles;
+                    break;
+                }
+                here = true;
             }
-            break;
-        }
-        const TileDesc dsc = sdesc[s];
-        while (fin_next < dsc.pair) {
-            finalize(fin_next, st_pair == fin_next);
-            ++fin_next;
-        }
-        st_pair = dsc.pair;
-        const bool half = Q8 && dsc.kind == kDeep;
-        if (!C::WIDE && st_half != (half ? 1 : 0)) load_q(half);
-        const uint32_t base = stage0 + s * C::STAGE_BYTES;
-        // mask-free: deepest-plane rows outside a draft window, or a full ring tile that every query of
-        // the call sees whole (one loop; every key before the first query and in the last one's window)
-        const int last = dsc.T + pa.j0 + a.qB - 1;
-        const bool whole =
-            dsc.kind == kDeep ? pa.dwin < 0
-                              : dsc.kind == kRing && ring_all_visible && dsc.t0 + kTileRows - 1 <= dsc.T + pa.j0 &&
-                                    (pa.all_deepest || pa.crel || dsc.t0 >= last - pa.W);
-        if constexpr (Q8) {
-            if (half) {
-                for (int b = 0; b < (dsc.cnt >> 6); ++b) {
-                    const uint32_t rb = base + b * q8_record_bytes(D);
-                    if (whole)
-                        block(dsc, rb, dsc.t0 + 64 * b, 64, std::true_type(), std::true_type());
-                    else
-                        block(dsc, rb, dsc.t0 + 64 * b, 64, std::false_type(), std::true_type());
+            const TileDesc dsc = sdesc[s];
+            if (dsc.pair != p) break;
+            const bool half = Q8 && dsc.kind == kDeep;
+            if (!C::WIDE && st_half != (half ? 1 : 0)) load_q(half);
+            const uint32_t base = stage0 + s * C::STAGE_BYTES;
+            // mask-free: deepest-plane rows outside a draft window, or a full ring tile that every query of
+            // the call sees whole (one loop; every key before the first query and in the last one's window)
+            const int last = dsc.T + pa.j0 + a.qB - 1;
+            const bool whole =
+                dsc.kind == kDeep ? pa.dwin < 0
+                                  : dsc.kind == kRing && ring_all_visible && dsc.t0 + kTileRows - 1 <= dsc.T + pa.j0 &&
+                                        (pa.all_deepest || pa.crel || dsc.t0 >= last - pa.W);
+            if constexpr (Q8) {
+                if (half) {
+                    for (int b = 0; b < (dsc.cnt >> 6); ++b) {
+                        const uint32_t rb = base + b * q8_record_bytes(D);
+                        if (whole)
+                            block(dsc, rb, dsc.t0 + 64 * b, 64, std::true_type(), std::true_type());
+                        else
+                            block(dsc, rb, dsc.t0 + 64 * b, 64, std::false_type(), std::true_type());
+                    }
                 }
             }
+            if (!half) {
+                if (!Q8 && whole && dsc.cnt == kTileRows)
+                    block(dsc, base, dsc.t0, dsc.cnt, std::true_type(), std::false_type());
+                else
+                    block(dsc, base, dsc.t0, dsc.cnt, std::false_type(), std::false_type());
+            }
+            if (C::WIDE && aborted) {
+                i = ntiles;
+                break;
+            }
+            publish();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty0 + 8 * s);
+            here = false;
+            i += TG;
         }
-        if (!half) {
-            if (!Q8 && whole && dsc.cnt == kTileRows)
-                block(dsc, base, dsc.t0, dsc.cnt, std::true_type(), std::false_type());
-            else
-                block(dsc, base, dsc.t0, dsc.cnt, std::false_type(), std::false_type());
-        }
-        if (C::WIDE && aborted) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty0 + 8 * s);
+        if (p < P_last) fetch_q(p + 1);
+        finalize(p);
     }
-    while (fin_next <= P_last) {
-        finalize(fin_next, !aborted && st_pair == fin_next);
-        ++fin_next;
-    }
+    publish();
     named_bar_sync(1, nct);
     if (*reinterpret_cast<volatile int *>(&sflag[1]) == 0) {
         const int nm = sflag[3];

@@ -41,6 +41,8 @@ int main(int argc, char **) {
         p.ring_box = S < kTileRows ? S : kTileRows;
         if (wide && p.ring_box > kWideRingRows) p.ring_box = kWideRingRows;
         p.deep_tile = unit > 1 && !wide ? 2 * kQ8Block : kTileRows;
+        p.ring_cost = 2;
+        p.head_cost = 2;
         p.crel = mode;
         p.sink = sink;
         p.dwin = window;
