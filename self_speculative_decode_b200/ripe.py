@@ -122,39 +122,55 @@ def _check(status: int, where: str):
         raise RipeError(status, where)
 
 
+_torch = None
+
+
+def _load_torch():
+    """torch, imported at the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream(stream):
-    import torch
+    """The raw handle of a stream: the current one, a torch stream or an int."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        torch = _torch or _load_torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _dev(t, dtype, shape, name):
-    import torch
+    """Address of a contiguous CUDA tensor of this dtype and (unless None) shape."""
+    torch = _torch or _load_torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _rows(t, dtype, shape, name):
-    """Pointer and token stride (elements) of a [N][B][heads][d] tensor whose heads are packed and whose tokens
+    """Address and token stride (elements) of a [N][B][heads][d] tensor whose heads are packed and whose tokens
     lie at one stride, as a part of a projection's output does."""
-    import torch
+    torch = _torch or _load_torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     N, B, H, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * d
     s = t.stride()
     # the stride of a dimension of one element says nothing
     ld = s[1] if B > 1 else s[0] if N > 1 else H * d
@@ -185,42 +201,42 @@ def ripe_cache_free(h):
 
 def ripe_load_prefix(h, layer, plane, T, k, v, ld_t, stream=None):
     n = len(T)
-    _check(lib().ripe_load_prefix(h, layer, plane, _ints(T, n), ctypes.c_void_p(k), ctypes.c_void_p(v),
+    _check(lib().ripe_load_prefix(h, layer, plane, _ints(T, n), k, v,
                                   ld_t, _stream(stream)), "ripe_load_prefix")
 
 
 def ripe_append_block(h, layer, r, B, k, v, stream=None):
-    _check(lib().ripe_append_block(h, layer, r, B, ctypes.c_void_p(k), ctypes.c_void_p(v), _stream(stream)),
+    _check(lib().ripe_append_block(h, layer, r, B, k, v, _stream(stream)),
            "ripe_append_block")
 
 
 def ripe_verify_attn(h, layer, r, q, out, lse=None, scale=1.0, stream=None):
-    _check(lib().ripe_verify_attn(h, layer, r, ctypes.c_void_p(q), ctypes.c_void_p(out),
-                                  ctypes.c_void_p(lse or 0), float(scale), _stream(stream)),
+    _check(lib().ripe_verify_attn(h, layer, r, q, out,
+                                  lse or None, float(scale), _stream(stream)),
            "ripe_verify_attn")
 
 
 def ripe_append_verify(h, layer, r, B, k, v, q, out, lse=None, scale=1.0, stream=None):
-    _check(lib().ripe_append_verify(h, layer, r, B, ctypes.c_void_p(k), ctypes.c_void_p(v), ctypes.c_void_p(q),
-                                    ctypes.c_void_p(out), ctypes.c_void_p(lse or 0), float(scale),
+    _check(lib().ripe_append_verify(h, layer, r, B, k, v, q,
+                                    out, lse or None, float(scale),
                                     _stream(stream)), "ripe_append_verify")
 
 
 def ripe_draft_attn(h, layer, r, j, k, v, q, out, lse=None, scale=1.0, stream=None):
-    _check(lib().ripe_draft_attn(h, layer, r, j, ctypes.c_void_p(k), ctypes.c_void_p(v), ctypes.c_void_p(q),
-                                 ctypes.c_void_p(out), ctypes.c_void_p(lse or 0), float(scale),
+    _check(lib().ripe_draft_attn(h, layer, r, j, k, v, q,
+                                 out, lse or None, float(scale),
                                  _stream(stream)), "ripe_draft_attn")
 
 
 def ripe_draft_attn_window(h, layer, r, j, sink, window, k, v, q, out, lse=None, scale=1.0, stream=None):
-    _check(lib().ripe_draft_attn_window(h, layer, r, j, int(sink), int(window), ctypes.c_void_p(k), ctypes.c_void_p(v),
-                                        ctypes.c_void_p(q), ctypes.c_void_p(out), ctypes.c_void_p(lse or 0),
+    _check(lib().ripe_draft_attn_window(h, layer, r, j, int(sink), int(window), k, v,
+                                        q, out, lse or None,
                                         float(scale), _stream(stream)), "ripe_draft_attn_window")
 
 
 def ripe_verify_attn_wave(h, layer, loop_of_position, q, out, lse=None, scale=1.0, stream=None):
     _check(lib().ripe_verify_attn_wave(h, layer, _ints(loop_of_position, len(loop_of_position)),
-                                       ctypes.c_void_p(q), ctypes.c_void_p(out), ctypes.c_void_p(lse or 0),
+                                       q, out, lse or None,
                                        float(scale), _stream(stream)), "ripe_verify_attn_wave")
 
 
@@ -229,7 +245,7 @@ def ripe_commit(h, accepted_len, stream=None):
 
 
 def ripe_commit_device(h, accepted_ptr, stream=None):
-    _check(lib().ripe_commit_device(h, ctypes.c_void_p(accepted_ptr), _stream(stream)), "ripe_commit_device")
+    _check(lib().ripe_commit_device(h, accepted_ptr, _stream(stream)), "ripe_commit_device")
 
 
 def ripe_sync_lengths(h, n, stream=None):
@@ -245,8 +261,8 @@ def ripe_cache_stats(h):
 
 
 def ripe_cache_export(h, n, layer, k_out, v_out, present, stream=None):
-    _check(lib().ripe_cache_export(h, n, layer, ctypes.c_void_p(k_out), ctypes.c_void_p(v_out),
-                                   ctypes.c_void_p(present), _stream(stream)), "ripe_cache_export")
+    _check(lib().ripe_cache_export(h, n, layer, k_out, v_out,
+                                   present, _stream(stream)), "ripe_cache_export")
 
 
 def ripe_get_device_error(h, stream=None):
@@ -257,9 +273,9 @@ def ripe_get_device_error(h, stream=None):
 
 def ripe_verify_attn_static(view, layer, r, q, out, lse=None, scale=1.0, device_error=None, stream=None):
     """Allocation-free verify over caller-owned buffers (see include/ripe.h); pointers are ints."""
-    _check(lib().ripe_verify_attn_static(ctypes.byref(view), layer, r, ctypes.c_void_p(q), ctypes.c_void_p(out),
-                                         ctypes.c_void_p(lse or 0), float(scale),
-                                         ctypes.c_void_p(device_error or 0), _stream(stream)),
+    _check(lib().ripe_verify_attn_static(ctypes.byref(view), layer, r, q, out,
+                                         lse or None, float(scale),
+                                         device_error or None, _stream(stream)),
            "ripe_verify_attn_static")
 
 
@@ -278,8 +294,8 @@ def ripe_cache_kv_bits(h):
 
 
 def ripe_cache_export_q8(h, n, layer, k_out, v_out, k_scale, v_scale, stream=None):
-    _check(lib().ripe_cache_export_q8(h, n, layer, ctypes.c_void_p(k_out), ctypes.c_void_p(v_out),
-                                      ctypes.c_void_p(k_scale), ctypes.c_void_p(v_scale), _stream(stream)),
+    _check(lib().ripe_cache_export_q8(h, n, layer, k_out, v_out,
+                                      k_scale, v_scale, _stream(stream)),
            "ripe_cache_export_q8")
 
 
@@ -290,23 +306,23 @@ def ripe_set_scores(h, softcap=0.0, slopes=None, stream=None):
 
 
 def ripe_append_block_rope(h, layer, r, B, k, v, ld_kv, q, ld_q, q_out, rope, stream=None):
-    _check(lib().ripe_append_block_rope(h, layer, r, B, ctypes.c_void_p(k), ctypes.c_void_p(v), ld_kv,
-                                        ctypes.c_void_p(q or 0), ld_q, ctypes.c_void_p(q_out or 0),
+    _check(lib().ripe_append_block_rope(h, layer, r, B, k, v, ld_kv,
+                                        q or None, ld_q, q_out or None,
                                         ctypes.byref(rope), _stream(stream)), "ripe_append_block_rope")
 
 
 def ripe_rotate_block(h, j, B, k, ld_k, k_out, q, ld_q, q_out, rope, stream=None):
-    _check(lib().ripe_rotate_block(h, j, B, ctypes.c_void_p(k or 0), ld_k, ctypes.c_void_p(k_out or 0),
-                                   ctypes.c_void_p(q or 0), ld_q, ctypes.c_void_p(q_out or 0), ctypes.byref(rope),
+    _check(lib().ripe_rotate_block(h, j, B, k or None, ld_k, k_out or None,
+                                   q or None, ld_q, q_out or None, ctypes.byref(rope),
                                    _stream(stream)), "ripe_rotate_block")
 
 
 def ripe_append_rope_static(view, layer, r, k, v, ld_kv, q, ld_q, q_out, rope, device_error, stream=None):
     """Append over caller-owned buffers (see include/ripe.h); pointers are ints, rope a Rope or None."""
-    _check(lib().ripe_append_rope_static(ctypes.byref(view), layer, r, ctypes.c_void_p(k), ctypes.c_void_p(v), ld_kv,
-                                         ctypes.c_void_p(q or 0), ld_q, ctypes.c_void_p(q_out or 0),
+    _check(lib().ripe_append_rope_static(ctypes.byref(view), layer, r, k, v, ld_kv,
+                                         q or None, ld_q, q_out or None,
                                          None if rope is None else ctypes.byref(rope),
-                                         ctypes.c_void_p(device_error), _stream(stream)), "ripe_append_rope_static")
+                                         device_error, _stream(stream)), "ripe_append_rope_static")
 
 
 def ripe_launch_count(h):
@@ -336,12 +352,12 @@ class RotaryTable:
     ``interleaved``: a pair is elements 2 i and 2 i + 1 of a head; else i and rotary_dim / 2 + i."""
 
     def __init__(self, cos, sin, interleaved=False):
-        import torch
+        torch = _torch or _load_torch()
         if cos.dim() != 2:
             raise ValueError("cos must be [positions][rotary_dim / 2]")
         self.cos, self.sin = cos, sin  # the struct below points into them
-        self.rope = Rope(cos=_dev(cos, torch.float32, None, "cos").value,
-                         sin=_dev(sin, torch.float32, cos.shape, "sin").value, positions=cos.shape[0],
+        self.rope = Rope(cos=_dev(cos, torch.float32, None, "cos"),
+                         sin=_dev(sin, torch.float32, cos.shape, "sin"), positions=cos.shape[0],
                          rotary_dim=2 * cos.shape[1], interleaved=1 if interleaved else 0)
 
 
@@ -349,7 +365,7 @@ def append_rope_static(view, layer, r, k, v, q=None, table=None, q_out=None, dev
     """ripe_append_rope_static with tensors: k, v [N][B][kvH][d] and q [N][B][Hq][d] (tokens may be strided) into the
     ring of ``view`` (a CacheView) and into ``q_out``, which is returned.  ``table``: a RotaryTable, or None to copy
     without rotating.  ``device_error``: an int32 tensor of one element that collects RIPE_DEVERR_* bits."""
-    import torch
+    torch = _torch or _load_torch()
     N, B = view.batch, view.block_len
     kp, ld_kv = _rows(k, torch.bfloat16, (N, B, view.kv_heads, view.head_dim), "k")
     vp, ld_v = _rows(v, torch.bfloat16, (N, B, view.kv_heads, view.head_dim), "v")
@@ -357,15 +373,19 @@ def append_rope_static(view, layer, r, k, v, q=None, table=None, q_out=None, dev
         raise ValueError("k and v must have the same token stride")
     if device_error is None:
         raise ValueError("device_error must be given")
+    here = torch.cuda.current_device()
+    for t in (k, v, q, q_out, device_error, table and table.cos, table and table.sin):
+        if t is not None and t.device.index != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
     qp, ld_q, qo = None, 0, None
     if q is not None:
         shape = (N, B, view.q_heads, view.head_dim)
         qp, ld_q = _rows(q, torch.bfloat16, shape, "q")
         if q_out is None:
             q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-        qo = _dev(q_out, torch.bfloat16, shape, "q_out").value
+        qo = _dev(q_out, torch.bfloat16, shape, "q_out")
     ripe_append_rope_static(view, layer, r, kp, vp, ld_kv, qp, ld_q, qo, None if table is None else table.rope,
-                            _dev(device_error, torch.int32, (1,), "device_error").value, stream)
+                            _dev(device_error, torch.int32, (1,), "device_error"), stream)
     return q_out
 
 
@@ -382,16 +402,25 @@ class RipeCache:
 
     def __init__(self, batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T, max_B,
                  window_mode=RIPE_WINDOW_QUERY_RELATIVE, kv_bits=16):
-        import torch
+        torch = _load_torch()
         if kv_bits not in (8, 16):
             raise ValueError("kv_bits must be 8 or 16")
         if not torch.cuda.is_available():
             raise RuntimeError("RipeCache needs a CUDA device")
         self.N, self.L, self.Hq, self.kvH, self.d = batch, layers, q_heads, kv_heads, head_dim
         self.R, self.W, self.max_T, self.max_B, self.mode = loops, window, max_T, max_B, window_mode
-        self.kv_bits = kv_bits
+        self.kv_bits, self.device = kv_bits, torch.cuda.current_device()
         self.handle = (ripe_cache_alloc if kv_bits == 16 else ripe_cache_alloc_q8)(
             batch, layers, q_heads, kv_heads, head_dim, loops, window, max_T, max_B, window_mode)
+
+    def _on(self, stream):
+        """The stream of a call: the one given, or the current one of the cache's device."""
+        return _torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream
+
+    def _here(self, *tensors):
+        for t in tensors:
+            if t is not None and t.device.index != self.device:
+                raise ValueError(f"a tensor is on {t.device}, the cache on cuda:{self.device}")
 
     def close(self):
         if self.handle is not None and self.handle.value:
@@ -405,18 +434,18 @@ class RipeCache:
             pass
 
     def load_prefix(self, layer, plane, T, k, v, stream=None):
-        import torch
+        torch = _torch or _load_torch()
         ld_t = k.shape[2]
         shape = (self.N, self.kvH, ld_t, self.d)
-        ripe_load_prefix(self.handle, layer, plane, list(T), _dev(k, torch.bfloat16, shape, "k").value,
-                         _dev(v, torch.bfloat16, shape, "v").value, ld_t, stream)
+        ripe_load_prefix(self.handle, layer, plane, list(T), _dev(k, torch.bfloat16, shape, "k"),
+                         _dev(v, torch.bfloat16, shape, "v"), ld_t, self._on(stream))
 
     def append_block(self, layer, r, k, v, stream=None):
-        import torch
+        torch = _torch or _load_torch()
         B = k.shape[1]
         shape = (self.N, B, self.kvH, self.d)
-        ripe_append_block(self.handle, layer, r, B, _dev(k, torch.bfloat16, shape, "k").value,
-                          _dev(v, torch.bfloat16, shape, "v").value, stream)
+        ripe_append_block(self.handle, layer, r, B, _dev(k, torch.bfloat16, shape, "k"),
+                          _dev(v, torch.bfloat16, shape, "v"), self._on(stream))
 
     def set_scores(self, softcap=0.0, slopes=None, stream=None):
         """Capped scores (softcap > 0) and a bias -slopes[h] * distance (Hq floats) in every later attention call."""
@@ -424,19 +453,20 @@ class RipeCache:
             slopes = slopes.tolist() if hasattr(slopes, "tolist") else list(slopes)
             if len(slopes) != self.Hq:
                 raise ValueError(f"expected {self.Hq} slopes")
-        ripe_set_scores(self.handle, softcap, slopes, stream)
+        ripe_set_scores(self.handle, softcap, slopes, self._on(stream))
 
     def append_block_rope(self, layer, r, k, v, table, q=None, q_out=None, stream=None):
         """append_block with k, and q if given, rotated by their positions; k, v and q may be parts of one projection's
         output (tokens strided).  Returns q_out."""
-        import torch
+        torch = _torch or _load_torch()
         B = k.shape[1]
         kp, ld_kv = _rows(k, torch.bfloat16, (self.N, B, self.kvH, self.d), "k")
         vp, ld_v = _rows(v, torch.bfloat16, (self.N, B, self.kvH, self.d), "v")
         if ld_v != ld_kv:
             raise ValueError("k and v must have the same token stride")
         qp, ld_q, q_out, qo = self._rotated(q, q_out, B, self.Hq, "q")
-        ripe_append_block_rope(self.handle, layer, r, B, kp, vp, ld_kv, qp, ld_q, qo, table.rope, stream)
+        self._here(k, v, q, q_out, table.cos, table.sin)
+        ripe_append_block_rope(self.handle, layer, r, B, kp, vp, ld_kv, qp, ld_q, qo, table.rope, self._on(stream))
         return q_out
 
     def rotate_block(self, j, table, k=None, q=None, k_out=None, q_out=None, stream=None):
@@ -445,45 +475,46 @@ class RipeCache:
         B = (k if k is not None else q).shape[1]
         kp, ld_k, k_out, ko = self._rotated(k, k_out, B, self.kvH, "k")
         qp, ld_q, q_out, qo = self._rotated(q, q_out, B, self.Hq, "q")
-        ripe_rotate_block(self.handle, j, B, kp, ld_k, ko, qp, ld_q, qo, table.rope, stream)
+        self._here(k, q, k_out, q_out, table.cos, table.sin)
+        ripe_rotate_block(self.handle, j, B, kp, ld_k, ko, qp, ld_q, qo, table.rope, self._on(stream))
         return k_out, q_out
 
     def _rotated(self, x, x_out, B, heads, name):
-        import torch
+        torch = _torch or _load_torch()
         if x is None:
             return None, 0, None, None
         shape = (self.N, B, heads, self.d)
         p, ld = _rows(x, torch.bfloat16, shape, name)
         if x_out is None:
             x_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-        return p, ld, x_out, _dev(x_out, torch.bfloat16, shape, name + "_out").value
+        return p, ld, x_out, _dev(x_out, torch.bfloat16, shape, name + "_out")
 
     def verify_attn(self, layer, r, q, out=None, lse=None, scale=1.0, stream=None):
-        import torch
+        torch = _torch or _load_torch()
         B = q.shape[1]
         shape = (self.N, B, self.Hq, self.d)
-        qp = _dev(q, torch.bfloat16, shape, "q").value
+        qp = _dev(q, torch.bfloat16, shape, "q")
         if out is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-        op = _dev(out, torch.bfloat16, shape, "out").value
-        lp = _dev(lse, torch.float32, shape[:3], "lse").value if lse is not None else None
-        ripe_verify_attn(self.handle, layer, r, qp, op, lp, scale, stream)
+        op = _dev(out, torch.bfloat16, shape, "out")
+        lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
+        ripe_verify_attn(self.handle, layer, r, qp, op, lp, scale, self._on(stream))
         return out
 
     def append_verify(self, layer, r, k, v, q, out=None, lse=None, scale=1.0, stream=None):
         """append_block(layer, r, k, v) + verify_attn(layer, r, q) in one launch."""
-        import torch
+        torch = _torch or _load_torch()
         B = q.shape[1]
         kshape = (self.N, B, self.kvH, self.d)
         shape = (self.N, B, self.Hq, self.d)
-        kp = _dev(k, torch.bfloat16, kshape, "k").value
-        vp = _dev(v, torch.bfloat16, kshape, "v").value
-        qp = _dev(q, torch.bfloat16, shape, "q").value
+        kp = _dev(k, torch.bfloat16, kshape, "k")
+        vp = _dev(v, torch.bfloat16, kshape, "v")
+        qp = _dev(q, torch.bfloat16, shape, "q")
         if out is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-        op = _dev(out, torch.bfloat16, shape, "out").value
-        lp = _dev(lse, torch.float32, shape[:3], "lse").value if lse is not None else None
-        ripe_append_verify(self.handle, layer, r, B, kp, vp, qp, op, lp, scale, stream)
+        op = _dev(out, torch.bfloat16, shape, "out")
+        lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
+        ripe_append_verify(self.handle, layer, r, B, kp, vp, qp, op, lp, scale, self._on(stream))
         return out
 
     def draft_attn(self, layer, r, j, k, v, q, out=None, lse=None, scale=1.0, stream=None, sink=None,
@@ -491,52 +522,52 @@ class RipeCache:
         """Draft step: write plane r of block position j (k, v [N][1][kvH][d]) and attend its
         query q [N][1][Hq][d] over keys up to that position; with ``sink`` / ``window`` only
         over the first ``sink`` keys and the last ``window`` + 1 (windowed draft attention)."""
-        import torch
+        torch = _torch or _load_torch()
         kshape = (self.N, 1, self.kvH, self.d)
         shape = (self.N, 1, self.Hq, self.d)
-        kp = _dev(k, torch.bfloat16, kshape, "k").value
-        vp = _dev(v, torch.bfloat16, kshape, "v").value
-        qp = _dev(q, torch.bfloat16, shape, "q").value
+        kp = _dev(k, torch.bfloat16, kshape, "k")
+        vp = _dev(v, torch.bfloat16, kshape, "v")
+        qp = _dev(q, torch.bfloat16, shape, "q")
         if out is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-        op = _dev(out, torch.bfloat16, shape, "out").value
-        lp = _dev(lse, torch.float32, shape[:3], "lse").value if lse is not None else None
+        op = _dev(out, torch.bfloat16, shape, "out")
+        lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
         if sink is None and window is None:
-            ripe_draft_attn(self.handle, layer, r, j, kp, vp, qp, op, lp, scale, stream)
+            ripe_draft_attn(self.handle, layer, r, j, kp, vp, qp, op, lp, scale, self._on(stream))
         else:
             ripe_draft_attn_window(self.handle, layer, r, j, 0 if sink is None else sink,
-                                   (1 << 30) if window is None else window, kp, vp, qp, op, lp, scale, stream)
+                                   (1 << 30) if window is None else window, kp, vp, qp, op, lp, scale, self._on(stream))
         return out
 
     def verify_attn_wave(self, layer, loop_of_position, q, out=None, lse=None, scale=1.0, stream=None):
         """Block position j verified at loop loop_of_position[j] (one pass over the deepest plane)."""
-        import torch
+        torch = _torch or _load_torch()
         B = q.shape[1]
         shape = (self.N, B, self.Hq, self.d)
-        qp = _dev(q, torch.bfloat16, shape, "q").value
+        qp = _dev(q, torch.bfloat16, shape, "q")
         if out is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-        op = _dev(out, torch.bfloat16, shape, "out").value
-        lp = _dev(lse, torch.float32, shape[:3], "lse").value if lse is not None else None
-        ripe_verify_attn_wave(self.handle, layer, list(loop_of_position), qp, op, lp, scale, stream)
+        op = _dev(out, torch.bfloat16, shape, "out")
+        lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
+        ripe_verify_attn_wave(self.handle, layer, list(loop_of_position), qp, op, lp, scale, self._on(stream))
         return out
 
     def commit(self, accepted_len, stream=None):
-        ripe_commit(self.handle, list(accepted_len), stream)
+        ripe_commit(self.handle, list(accepted_len), self._on(stream))
 
     def commit_device(self, accepted, stream=None):
-        import torch
-        ripe_commit_device(self.handle, _dev(accepted, torch.int32, (self.N,), "accepted").value, stream)
+        torch = _torch or _load_torch()
+        ripe_commit_device(self.handle, _dev(accepted, torch.int32, (self.N,), "accepted"), self._on(stream))
 
     def sync_lengths(self, stream=None):
-        return ripe_sync_lengths(self.handle, self.N, stream)
+        return ripe_sync_lengths(self.handle, self.N, self._on(stream))
 
     def stats(self):
         return ripe_cache_stats(self.handle)
 
     def export(self, n, layer, stream=None):
         """Logical view of sequence n, layer: (k, v [R][kvH][Tv][d] bf16, present [R][Tv] uint8)."""
-        import torch
+        torch = _torch or _load_torch()
         st = self.stats()
         if not st["lengths_synced"]:
             raise RipeError(RIPE_ESTATE, "export")
@@ -546,12 +577,12 @@ class RipeCache:
         v = torch.zeros_like(k)
         present = torch.zeros((self.R, Tv), dtype=torch.uint8, device=dev)
         if Tv:
-            ripe_cache_export(self.handle, n, layer, k.data_ptr(), v.data_ptr(), present.data_ptr(), stream)
+            ripe_cache_export(self.handle, n, layer, k.data_ptr(), v.data_ptr(), present.data_ptr(), self._on(stream))
         return k, v, present
 
     def export_q8(self, n, layer, stream=None):
         """8-bit blocks of sequence n, layer: k, v int8 [kvH][D][d] and their scales fp32 [kvH][D / 64]."""
-        import torch
+        torch = _torch or _load_torch()
         if not self.stats()["lengths_synced"]:
             raise RipeError(RIPE_ESTATE, "export_q8")
         blocks = max(0, self.sync_lengths(stream)[n] - self.W) // 64
@@ -559,11 +590,11 @@ class RipeCache:
         k, v = (torch.empty((self.kvH, 64 * blocks, self.d), dtype=torch.int8, device=dev) for _ in range(2))
         ks, vs = (torch.empty((self.kvH, blocks), dtype=torch.float32, device=dev) for _ in range(2))
         if blocks or self.kv_bits != 8:
-            ripe_cache_export_q8(self.handle, n, layer, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), stream)
+            ripe_cache_export_q8(self.handle, n, layer, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), self._on(stream))
         return k, v, ks, vs
 
     def device_error(self, stream=None):
-        return ripe_get_device_error(self.handle, stream)
+        return ripe_get_device_error(self.handle, self._on(stream))
 
     def launch_count(self):
         return ripe_launch_count(self.handle)
