@@ -27,12 +27,15 @@ __device__ __forceinline__ size_t deep_row(int layer, int n, int kh, int t, int 
 __global__ void ripe_append_kernel(uint4 *__restrict__ Kw, uint4 *__restrict__ Vw,
                                    const uint4 *__restrict__ k, const uint4 *__restrict__ v,
                                    const int32_t *__restrict__ T, uint32_t *err, int N, int B, int kvH,
-                                   int d8, int R, int S, int layer, int r, int max_T) {
+                                   int d8, int R, int S, int layer, int r, int max_T, int early) {
     // The next launch may start at once: a verify launch reads nothing this kernel writes before
     // its own wait, which returns only after this kernel (and so its predecessor) has completed.
     // Its CTAs then take the SMs that the previous verify launch leaves, while this one waits.
-    pdl_trigger();
+    // Not so behind a launch that writes the lengths or the deepest-plane region (a commit), both of which a
+    // verify launch reads at its start: it may then begin only once that launch has completed.
+    if (early) pdl_trigger();
     pdl_wait();
+    if (!early) pdl_trigger();
     const size_t total = static_cast<size_t>(N) * B * kvH * d8;
     for (size_t idx = blockIdx.x * static_cast<size_t>(blockDim.x) + threadIdx.x; idx < total;
          idx += static_cast<size_t>(gridDim.x) * blockDim.x) {
@@ -63,7 +66,7 @@ int launch_append(ripe_cache *c, int layer, int r, int B, const void *k, const v
     launch_pdl(ripe_append_kernel, dim3(blocks), dim3(256), 0, s, reinterpret_cast<uint4 *>(c->Kw),
                reinterpret_cast<uint4 *>(c->Vw), static_cast<const uint4 *>(k), static_cast<const uint4 *>(v),
                static_cast<const int32_t *>(c->T_dev), c->err_dev, c->N, B, c->kvH, d8, c->R, c->ring_slots, layer,
-               r, c->max_T);
+               r, c->max_T, c->lengths_dirty ? 0 : 1);
     c->launches += 1;
     c->lengths_dirty = false;
     return cudaGetLastError() == cudaSuccess ? RIPE_OK : RIPE_ECUDA;
