@@ -75,14 +75,15 @@ struct SCfg {
     // Q in fragment order, [form][row tile][D / 32][lane] of 16 bytes: bf16, and f16 for 8-bit tiles
     static constexpr int QF_BYTES = ROWS * D * 2;
     static constexpr int Q_BYTES = (Q8 ? 2 : 1) * QF_BYTES;
-    // WIDE: P in fragment order, [group][2][16-key sub-block][pair of row tiles][lane] of 16 bytes
+    // WIDE: P, [group][2][16-key sub-block][row tile] of two 8 x 8 matrices
     static constexpr int P_BYTES = WIDE ? TG * 2 * 4 * (NQT / 2) * 512 : 0;
     // merge buffer: rows of o per warp, or per group of a wide one; (m, l_out, l_lse) per warp
     static constexpr int DP = D + 4;
     static constexpr int SLOTS = WIDE ? TG : NCW;
     static constexpr int NPF = WIDE ? TG : NP;  // partials of a row of o
     static constexpr int MERGE_FLOATS = SLOTS * NQ * DP;
-    static constexpr int GM_FLOATS = WIDE ? NCW * NQ : 0;  // column maxima of a wide group's warps
+    // WIDE: column maxima and l_fix of each warp, references of each group
+    static constexpr int GM_FLOATS = WIDE ? (2 * NCW + TG) * NQ : 0;
     static constexpr int MLF = NCW * NQ * 4 + ROWS * (NPF + 4) + 3 * ROWS + GM_FLOATS + (WIDE ? 4 * TG : 0);
     static_assert(MLF % 4 == 0 && (ROWS * NPF) % 4 == 0, "alignment");
     static constexpr int MISC = 1024 + 1024;
@@ -107,8 +108,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 __device__ __forceinline__ void l2_prefetch(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
@@ -124,6 +125,24 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
 // D = A * B (+ D): f16 or bf16 operands, fp32 sums; the first product of a chain needs no zeroed registers
@@ -331,7 +350,9 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     float *qscale = fin + C::ROWS * 4;                                    // [ROWS] sx over the row's power of two
     float *qslope = qscale + C::ROWS;                                     // [ROWS] distance bias of the row's head
     int *qpos = reinterpret_cast<int *>(qslope + C::ROWS);                // [ROWS] block position, -1: no such row
-    float *gmax = reinterpret_cast<float *>(qpos + C::ROWS);              // [NCW][NQ] column maxima (WIDE)
+    float *gmax = reinterpret_cast<float *>(qpos + C::ROWS);              // WIDE [NCW][NQ] column maxima
+    float *gfix = gmax + C::NCW * C::NQ;                                  // WIDE [NCW][NQ] l_fix
+    float *gref = gfix + C::NCW * C::NQ;                                  // WIDE [TG][NQ] m_ref
     // WIDE [TG][4]: the last even and the last odd block that moves a reference; the group has given up; -
     int *gflag = reinterpret_cast<int *>(gmax + C::GM_FLOATS);
     uint64_t *bars = reinterpret_cast<uint64_t *>(mml + C::MLF);          // full[NS], empty[NS]
@@ -471,7 +492,8 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     float o[C::MT][NQT][4];
     // l_lse sums the probabilities in fp32; l_fix sums what rounding adds to them in bf16 tiles, where the P V
     // product sees 2^-8: the output is normalised by both together, which is what O sums.  A column's reference means nothing until some lane's l_lse is not zero
-    float m_ref[NQT][2], l_lse[NQT][2], l_fix[NQT][2];
+    // (WIDE: m_ref and l_fix are in shared memory, a column's by the lane with g4 == 0, to fit 128 registers)
+    float l_lse[NQT][2], m_ref[C::WIDE ? 1 : NQT][2], l_fix[C::WIDE ? 1 : NQT][2];
     uint32_t seen = 0;  // WIDE: bit 2 nq + e is set once the column has a reference
     uint32_t qb[C::WIDE ? 1 : D / 16][C::WIDE ? 1 : NQT][2];  // Q as B fragments
 
@@ -486,10 +508,21 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             for (int nq = 0; nq < NQT; ++nq) o[mt][nq][0] = o[mt][nq][1] = o[mt][nq][2] = o[mt][nq][3] = 0.f;
 #pragma unroll
         for (int nq = 0; nq < NQT; ++nq) {
-            m_ref[nq][0] = m_ref[nq][1] = 0.f;
             l_lse[nq][0] = l_lse[nq][1] = 0.f;
-            l_fix[nq][0] = l_fix[nq][1] = 0.f;
+            if constexpr (!C::WIDE) {
+                m_ref[nq][0] = m_ref[nq][1] = 0.f;
+                l_fix[nq][0] = l_fix[nq][1] = 0.f;
+            }
         }
+        if constexpr (C::WIDE) {  // (the barrier of stage_q follows)
+            gfix[warp * C::NQ + lane] = 0.f;
+            if (kg == 0) gref[tg * C::NQ + lane] = 0.f;
+        }
+    };
+    // references of columns 8 nq + 2 c4 and the next
+    auto refs = [&](int nq) -> float2 {
+        if constexpr (C::WIDE) return *reinterpret_cast<const float2 *>(&gref[tg * C::NQ + 8 * nq + 2 * c4]);
+        else return make_float2(m_ref[nq][0], m_ref[nq][1]);
     };
 
     // kv head of pair p, its first query row, and how many rows the pair has
@@ -567,14 +600,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     };
 
     // The CTAs holding tiles of pair p (x: the first of them, y: how many).  Only this CTA's first and last pair can be
-    // shared; one thread has looked them up.
-    if (tid == 32) {
-        const int2 f = score_parts(a, cp, cum, Ts, kvH, P_first), l = score_parts(a, cp, cum, Ts, kvH, P_last);
-        sflag[8] = f.x;
-        sflag[9] = f.y;
-        sflag[10] = l.x;
-        sflag[11] = l.y;
-    }
+    // shared; one thread looks them up at the start.
     auto parts_of = [&](int p) -> int2 {
         return p == P_first ? make_int2(sflag[8], sflag[9]) : p == P_last ? make_int2(sflag[10], sflag[11])
                                                                           : make_int2(static_cast<int>(blockIdx.x), 1);
@@ -628,16 +654,19 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         for (int nq = 0; nq < NQT; ++nq)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float l = l_lse[nq][e], lb = l_fix[nq][e];
+                float l = l_lse[nq][e], fix = 0.f;
+                if constexpr (!C::WIDE) fix = l_fix[nq][e];
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) {
                     l += __shfl_xor_sync(0xffffffffu, l, x);
-                    lb += __shfl_xor_sync(0xffffffffu, lb, x);
+                    if (!C::WIDE) fix += __shfl_xor_sync(0xffffffffu, fix, x);
                 }
+                if (C::WIDE) fix = gfix[warp * C::NQ + 8 * nq + 2 * c4 + e];
                 const bool none = C::WIDE ? !(seen >> (2 * nq + e) & 1) : l == 0.f;  // (the same for a wide group)
+                const float2 m = refs(nq);
                 if (g4 == 0)
                     *reinterpret_cast<float4 *>(&mml[(slot * C::NQ + 8 * nq + 2 * c4 + e) * 4]) =
-                        make_float4(none ? -INFINITY : m_ref[nq][e], l + lb, l, 0.f);
+                        make_float4(none ? -INFINITY : e ? m.y : m.x, l + fix, l, 0.f);
             }
         named_bar_sync(1, nct);
         const bool abort_now = *reinterpret_cast<volatile int *>(&sflag[1]) != 0;
@@ -694,6 +723,37 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     // Runs in the CTA that arrived last, after all of its own tiles (the stage buffers are free).
     auto merge_pair = [&](int p) {
         const int c_first = parts_of(p).x, nparts = parts_of(p).y, mq = rows_of(p);
+        constexpr int FEW = 4;
+        if (nparts <= FEW) {  // every thread weighs for itself: all loads in flight at once, no barrier
+            for (int e = tid; e < mq * (D / 4); e += nct) {
+                const int i = e / (D / 4), cx = e - (e / (D / 4)) * (D / 4);
+                float4 ml[FEW], v[FEW];
+#pragma unroll
+                for (int c = 0; c < FEW; ++c) {
+                    const size_t prow = (static_cast<size_t>(c_first + (c < nparts ? c : 0)) + p) * C::ROWS + i;
+                    ml[c] = __ldcg(reinterpret_cast<const float4 *>(&a.part_ml[prow * 4]));
+                    v[c] = __ldcg(reinterpret_cast<const float4 *>(&a.part_o[prow * D + 4 * cx]));
+                }
+                float M = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < FEW; ++c)
+                    if (c < nparts) M = fmaxf(M, ml[c].x);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float L = 0.f, Ll = 0.f;
+#pragma unroll
+                for (int c = 0; c < FEW; ++c) {
+                    const float w = c >= nparts || ml[c].x == -INFINITY ? 0.f : exp2f(ml[c].x - M);
+                    if (w != 0.f) {
+                        acc.x += w * v[c].x; acc.y += w * v[c].y; acc.z += w * v[c].z; acc.w += w * v[c].w;
+                        L += w * ml[c].y;
+                        Ll += w * ml[c].z;
+                    }
+                }
+                write_row(p, i, 4 * cx, acc, M, L, Ll);
+            }
+            if (tid == 0) a.counters[p] = 0;
+            return;
+        }
         float *pw = reinterpret_cast<float *>(stages);  // [nparts][ROWS] m, then weights
         float *pl = pw + nparts * C::ROWS;              // [nparts][ROWS] l
         for (int e = tid; e < nparts * mq; e += nct) {
@@ -805,12 +865,25 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         for (int nq = 0; nq < NQT; ++nq) {
             float2 qs = make_float2(0.f, 0.f);
             if (HALF) qs = *reinterpret_cast<const float2 *>(&qscale[col0 + 8 * nq]);
+            const float2 m = refs(nq);
+            if constexpr (FAST && HALF && !MOD) {
+                const float2 f = make_float2(qs.x * sc.ks, qs.y * sc.ks);
+                const float2 off = make_float2(sc.lv - m.x, sc.lv - m.y);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+                for (int sb = 0; sb < C::SB; ++sb)
+#pragma unroll
+                    for (int h = 0; h < 4; h += 2) {
+                        const float2 y = fma2(make_float2(x[sb][nq][h], x[sb][nq][h + 1]), f, off);
+                        x[sb][nq][h] = y.x;
+                        x[sb][nq][h + 1] = y.y;
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < (FAST && HALF && !MOD ? 0 : 2); ++e) {
                 const int col = col0 + 8 * nq + e;
                 const int jq = FAST && !MOD ? 0 : qpos[col];
                 const float f = HALF ? sc.ks * (e ? qs.y : qs.x) : a.sx;
-                const float off = HALF ? sc.lv - m_ref[nq][e] : -m_ref[nq][e];
+                const float off = HALF ? sc.lv - (e ? m.y : m.x) : -(e ? m.y : m.x);
                 // distance of this lane's first key from the query (exact below 2^24), and its visible range
                 const int first = t0 + 16 * kb1 + g4;
                 const float slope = MOD ? qslope[col] : 0.f;
@@ -846,28 +919,23 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         }
     };
 
-    // P of 16 keys as B fragments (keys x query columns); adds to the columns' sums
-    auto weigh = [&](const float (&x)[NQT][4], float (&tl)[NQT][2], float (&tr)[NQT][2], uint32_t (&pb)[NQT][2], auto half_tag) {
+    // P of 16 keys, rounded (rows g4 and g4 + 8, columns 2 c4 and 2 c4 + 1); adds to the columns' sums
+    auto weigh = [&](const float (&x)[4], float (&tl)[2], float (&tr)[2], uint32_t &lo, uint32_t &hi, auto half_tag) {
         constexpr bool HALF = decltype(half_tag)::value;
-#pragma unroll
-        for (int nq = 0; nq < NQT; ++nq) {
-            const float p0 = exp2f(x[nq][0]), p1 = exp2f(x[nq][1]), p2 = exp2f(x[nq][2]), p3 = exp2f(x[nq][3]);
-            tl[nq][0] += p0 + p2;
-            tl[nq][1] += p1 + p3;
-            uint32_t lo, hi;
-            if constexpr (HALF) {
-                const __half2 l2 = __floats2half2_rn(p0, p1), h2 = __floats2half2_rn(p2, p3);
-                lo = *reinterpret_cast<const uint32_t *>(&l2);
-                hi = *reinterpret_cast<const uint32_t *>(&h2);
-            } else {
-                const __nv_bfloat162 l2 = __floats2bfloat162_rn(p0, p1), h2 = __floats2bfloat162_rn(p2, p3);
-                tr[nq][0] += __low2float(l2) + __low2float(h2);
-                tr[nq][1] += __high2float(l2) + __high2float(h2);
-                lo = *reinterpret_cast<const uint32_t *>(&l2);
-                hi = *reinterpret_cast<const uint32_t *>(&h2);
-            }
-            pb[nq][0] = movmatrix_t(lo);
-            pb[nq][1] = movmatrix_t(hi);
+        const float2 p = make_float2(exp2f(x[0]), exp2f(x[1])), r = make_float2(exp2f(x[2]), exp2f(x[3]));
+        const float2 t = add2(make_float2(tl[0], tl[1]), add2(p, r));
+        tl[0] = t.x;
+        tl[1] = t.y;
+        if constexpr (HALF) {
+            const __half2 l2 = __floats2half2_rn(p.x, p.y), h2 = __floats2half2_rn(r.x, r.y);
+            lo = *reinterpret_cast<const uint32_t *>(&l2);
+            hi = *reinterpret_cast<const uint32_t *>(&h2);
+        } else {
+            const __nv_bfloat162 l2 = __floats2bfloat162_rn(p.x, p.y), h2 = __floats2bfloat162_rn(r.x, r.y);
+            tr[0] += __low2float(l2) + __low2float(h2);
+            tr[1] += __high2float(l2) + __high2float(h2);
+            lo = *reinterpret_cast<const uint32_t *>(&l2);
+            hi = *reinterpret_cast<const uint32_t *>(&h2);
         }
     };
 
@@ -960,21 +1028,46 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     // that reads as NaN takes nothing from it
     auto add_sums = [&](const float (&tl)[NQT][2], const float (&tr)[NQT][2], float iv, auto fast_tag, auto half_tag) {
         constexpr bool FAST = decltype(fast_tag)::value, HALF = decltype(half_tag)::value;
+        if constexpr (FAST && HALF) {
 #pragma unroll
-        for (int nq = 0; nq < NQT; ++nq)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float s = !HALF ? tl[nq][e] : !FAST && tl[nq][e] == 0.f ? 0.f : tl[nq][e] * iv;
-                l_lse[nq][e] += s;
-                if (!HALF) l_fix[nq][e] += tr[nq][e] - tl[nq][e];
+            for (int nq = 0; nq < NQT; ++nq) {
+                const float2 l = fma2(make_float2(tl[nq][0], tl[nq][1]), make_float2(iv, iv),
+                                      make_float2(l_lse[nq][0], l_lse[nq][1]));
+                l_lse[nq][0] = l.x;
+                l_lse[nq][1] = l.y;
             }
+        } else {
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float s = !HALF ? tl[nq][e] : !FAST && tl[nq][e] == 0.f ? 0.f : tl[nq][e] * iv;
+                    l_lse[nq][e] += s;
+                    if constexpr (!HALF) {
+                        float fix = tr[nq][e] - tl[nq][e];
+                        if constexpr (C::WIDE) {
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1) fix += __shfl_xor_sync(0xffffffffu, fix, x);
+                            if (g4 == 0) gfix[warp * C::NQ + 8 * nq + 2 * c4 + e] += fix;
+                        } else {
+                            l_fix[nq][e] += fix;
+                        }
+                    }
+                }
+        }
     };
 
     // moves a column's reference up by `up` (al: what its sums are worth then)
     auto move_ref = [&](int nq, int e, float up, float al, float (&x)[C::SB][NQT][4]) {
-        m_ref[nq][e] += up;
         l_lse[nq][e] *= al;
-        l_fix[nq][e] *= al;
+        if constexpr (C::WIDE) {
+            const int col = 8 * nq + 2 * c4 + e;
+            if (g4 == 0) gfix[warp * C::NQ + col] *= al;
+            if (g4 == 0 && kg == 0) gref[tg * C::NQ + col] += up;
+        } else {
+            m_ref[nq][e] += up;
+            l_fix[nq][e] *= al;
+        }
 #pragma unroll
         for (int sb = 0; sb < C::SB; ++sb) {
             x[sb][nq][e] -= up;
@@ -1041,7 +1134,13 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             const int kb = kg * C::SB + sb;
             if (!FAST && 16 * kb >= cnt) continue;
             uint32_t pb[NQT][2];
-            weigh(x[sb], tl, tr, pb, half_tag);
+#pragma unroll
+            for (int nq = 0; nq < NQT; ++nq) {
+                uint32_t lo, hi;
+                weigh(x[sb][nq], tl[nq], tr[nq], lo, hi, half_tag);
+                pb[nq][0] = movmatrix_t(lo);  // to the B operand's layout
+                pb[nq][1] = movmatrix_t(hi);
+            }
             accumulate(dsc, kb0, t0, cnt, kb, 0, pb, fast_tag, half_tag);
         }
         add_sums(tl, tr, sc.iv, fast_tag, half_tag);
@@ -1053,7 +1152,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     // is weighed again after its warps have compared their maxima.  P is double-buffered: a warp that writes the
     // buffer of block n + 2 has passed the barrier of block n + 1, which its readers reach after block n.
     int nblk = 0;
-    const uint32_t pbuf0 = smem_addr(qf) + C::Q_BYTES + tg * (C::P_BYTES / TG) + lane * 16;
+    const uint32_t pbuf0 = smem_addr(qf) + C::Q_BYTES + tg * (C::P_BYTES / TG);
     auto compute_wide = [&](const TileDesc &dsc, uint32_t kb0, int t0, int cnt, auto fast_tag, auto half_tag) {
         constexpr bool FAST = decltype(fast_tag)::value, HALF = decltype(half_tag)::value;
         constexpr int PT = (NQT / 2) * 512;  // bytes of P of a sub-block
@@ -1062,26 +1161,35 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         float x[C::SB][NQT][4], tl[NQT][2], tr[NQT][2];
         Scales sc = {1.f, 0.f, 1.f};
         if constexpr (HALF) sc = scales_of(kb0);
-        auto put = [&]() {
+        // P as 8 x 8 matrices of 128 bytes, rows keys, columns queries: [row tile][keys 0..7, 8..15], which ldmatrix
+        // transposes into B fragments.  Returns whether a probability exceeds 2^kScoreHi.
+        auto put = [&]() -> bool {
+            uint32_t most = 0;
 #pragma unroll
-            for (int nq = 0; nq < NQT; ++nq) tl[nq][0] = tl[nq][1] = tr[nq][0] = tr[nq][1] = 0.f;
-            uint32_t pb[NQT][2];
-            weigh(x[0], tl, tr, pb, half_tag);
-#pragma unroll
-            for (int i = 0; i < NQT / 2; ++i)
-                sts128(pbuf + kg * PT + i * 512,
-                       make_uint4(pb[2 * i][0], pb[2 * i][1], pb[2 * i + 1][0], pb[2 * i + 1][1]));
+            for (int nq = 0; nq < NQT; ++nq) {
+                tl[nq][0] = tl[nq][1] = tr[nq][0] = tr[nq][1] = 0.f;
+                uint32_t lo, hi;
+                weigh(x[0][nq], tl[nq], tr[nq], lo, hi, half_tag);
+                const uint32_t at = pbuf + kg * PT + nq * 256 + lane * 4;
+                sts32(at, lo);
+                sts32(at + 128, hi);
+                most = __vmaxu2(most, __vmaxu2(lo, hi));  // probabilities have no sign: ordered as their bits
+            }
+            const uint32_t bound = HALF ? 0x7800u : 0x4700u;  // 2^15 as f16, as bf16 (NaN is above both: harmless)
+            return (most & 0xFFFFu) > bound || (most >> 16) > bound;
         };
         if (mine) {
             scores(kb0, kg, x[0], half_tag);
             relative(dsc, t0, cnt, kg, sc, x, fast_tag, half_tag);
-            // (while some column has no reference yet, any score calls for the others' look)
-            float most = -INFINITY;
+            bool over = put();
+            if (seen != (1u << (2 * NQT)) - 1) {  // some column has no reference yet: any score of it calls for one
 #pragma unroll
-            for (int nq = 0; nq < NQT; ++nq) most = fmaxf(most, fmaxf(column_max(x, nq, 0), column_max(x, nq, 1)));
-            const bool over = most > (seen == (1u << (2 * NQT)) - 1 ? kScoreHi : -INFINITY);
+                for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        over = over || (!(seen >> (2 * nq + e) & 1) && column_max(x, nq, e) > -INFINITY);
+            }
             if (__any_sync(0xffffffffu, over) && lane == 0) gflag[4 * tg + (nblk & 1)] = nblk;
-            put();
         } else {
 #pragma unroll
             for (int nq = 0; nq < NQT; ++nq) {
@@ -1128,13 +1236,9 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                 if (!FAST && 16 * kb >= cnt) continue;
                 uint32_t pb[NQT][2];
 #pragma unroll
-                for (int i = 0; i < NQT / 2; ++i) {
-                    const uint4 w = lds128(pbuf + kb * PT + i * 512);
-                    pb[2 * i][0] = w.x;
-                    pb[2 * i][1] = w.y;
-                    pb[2 * i + 1][0] = w.z;
-                    pb[2 * i + 1][1] = w.w;
-                }
+                for (int i = 0; i < NQT / 2; ++i)
+                    ldsm_x4_t(pbuf + kb * PT + i * 512 + lane * 16, pb[2 * i][0], pb[2 * i][1], pb[2 * i + 1][0],
+                              pb[2 * i + 1][1]);
                 accumulate(dsc, kb0, t0, cnt, kb, C::MT * kg, pb, fast_tag, half_tag);
             }
         }
@@ -1153,6 +1257,13 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     bool here = false;  // tile i has landed
     if (a.early) pdl_wait();  // the caller may be writing the queries
     fetch_q(P_first);
+    if (tid == 32) {
+        const int2 f = score_parts(a, cp, cum, Ts, kvH, P_first), l = score_parts(a, cp, cum, Ts, kvH, P_last);
+        sflag[8] = f.x;
+        sflag[9] = f.y;
+        sflag[10] = l.x;
+        sflag[11] = l.y;
+    }
     for (int p = P_first; p <= P_last; ++p) {
         reset_state();
         stage_q(p);

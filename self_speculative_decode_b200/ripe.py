@@ -375,7 +375,7 @@ def append_rope_static(view, layer, r, k, v, q=None, table=None, q_out=None, dev
         raise ValueError("device_error must be given")
     here = torch.cuda.current_device()
     for t in (k, v, q, q_out, device_error, table and table.cos, table and table.sin):
-        if t is not None and t.device.index != here:
+        if t is not None and t.get_device() != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
     qp, ld_q, qo = None, 0, None
     if q is not None:
@@ -419,7 +419,7 @@ class RipeCache:
 
     def _here(self, *tensors):
         for t in tensors:
-            if t is not None and t.device.index != self.device:
+            if t is not None and t.get_device() != self.device:
                 raise ValueError(f"a tensor is on {t.device}, the cache on cuda:{self.device}")
 
     def close(self):
@@ -495,7 +495,7 @@ class RipeCache:
         shape = (self.N, B, self.Hq, self.d)
         qp = _dev(q, torch.bfloat16, shape, "q")
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            out = torch.empty_like(q)  # contiguous, as q
         op = _dev(out, torch.bfloat16, shape, "out")
         lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
         ripe_verify_attn(self.handle, layer, r, qp, op, lp, scale, self._on(stream))
@@ -511,7 +511,7 @@ class RipeCache:
         vp = _dev(v, torch.bfloat16, kshape, "v")
         qp = _dev(q, torch.bfloat16, shape, "q")
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            out = torch.empty_like(q)  # contiguous, as q
         op = _dev(out, torch.bfloat16, shape, "out")
         lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
         ripe_append_verify(self.handle, layer, r, B, kp, vp, qp, op, lp, scale, self._on(stream))
@@ -529,7 +529,7 @@ class RipeCache:
         vp = _dev(v, torch.bfloat16, kshape, "v")
         qp = _dev(q, torch.bfloat16, shape, "q")
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            out = torch.empty_like(q)  # contiguous, as q
         op = _dev(out, torch.bfloat16, shape, "out")
         lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
         if sink is None and window is None:
@@ -546,7 +546,7 @@ class RipeCache:
         shape = (self.N, B, self.Hq, self.d)
         qp = _dev(q, torch.bfloat16, shape, "q")
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            out = torch.empty_like(q)  # contiguous, as q
         op = _dev(out, torch.bfloat16, shape, "out")
         lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
         ripe_verify_attn_wave(self.handle, layer, list(loop_of_position), qp, op, lp, scale, self._on(stream))
