@@ -213,7 +213,8 @@ int ripe_rotate_block(ripe_cache_t *c, int j, int B, const void *k, int64_t ld_k
  * softcap 0 and slopes NULL (the state after allocation) give plain scores again.  Not while the
  * stream is captured (RIPE_ESTATE); a captured graph keeps the softcap and the presence of slopes that it
  * was captured with, and reads the slopes of the last call.  With either, the draft calls and
- * ripe_append_verify take two launches and q and out are 16-byte aligned (RIPE_EINVAL).
+ * ripe_append_verify take two launches, q and out are 16-byte aligned, and scale and scale / softcap are
+ * finite (RIPE_EINVAL).
  */
 int ripe_set_scores(ripe_cache_t *c, float softcap, const float *slopes, void *stream);
 

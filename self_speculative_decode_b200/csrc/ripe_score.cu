@@ -1,9 +1,10 @@
 // Launch of the attention over 8-bit caches or with capped or biased scores, and its instances over bf16
 // caches.
+#include <cmath>
+
 #include "ripe_score_kernel.cuh"
 
 namespace ripe {
-
 
 cudaError_t launch_score_bf16(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s) {
     switch (d) {
@@ -96,6 +97,7 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     const float log2e = 1.4426950408889634f;
     a.cap = c->softcap * log2e;
     a.sx = c->softcap > 0.f ? 2.f * call.scale * log2e / c->softcap : call.scale * log2e;
+    if (!std::isfinite(a.sx)) return RIPE_EINVAL;  // a scale, or a scale over a cap, that no score survives
     a.dbg_deep_rows = c->deep_rows;
     // partials of two groups of 32 rows take the room of one of 64 (ripe_cache_alloc's scratch)
     a.dbg_part_slots = c->num_sms + c->N * c->kvH * a.groups;

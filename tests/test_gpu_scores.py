@@ -93,6 +93,24 @@ def test_scores_are_set_and_cleared(cuda_device):
     p.close()
 
 
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("Hq,B", [(2, 3), (4, 4), (8, 6), (8, 8)])
+def test_a_query_with_nan_spoils_its_own_row_only(cuda_device, bits, Hq, B):
+    """And a log-sum-exp that is not asked for is not written."""
+    p = Pair(2, Hq, 1, 64, 2, 8, [300, 20], B, bits=bits, cap=25.0, seed=13).load().append(B)
+    qb = p.queries(B)
+    bad = qb.copy()
+    bad[0, 1, 0, 3] = 0x7FC0
+    bad[1, 0, 1, 5] = 0x7F80
+    out = p.gpu.verify_attn(0, 0, bits_dev(bad))
+    want = p.gpu.verify_attn(0, 0, bits_dev(qb))
+    spoilt = torch.zeros((2, B, Hq), dtype=torch.bool, device="cuda")
+    spoilt[0, 1, 0] = spoilt[1, 0, 1] = True
+    assert torch.equal(out[~spoilt], want[~spoilt])
+    assert out[0, 1, 0].isnan().all() and not torch.equal(out[1, 0, 1], want[1, 0, 1])
+    p.close()
+
+
 def test_two_caches_and_a_second_stream(cuda_device):
     """Two caches used in turn, one of them on a stream of its own."""
     a = Pair(2, 4, 2, 64, 2, 8, [200, 131], 3, bits=8, cap=20.0, seed=5).load().append(3)
@@ -134,4 +152,9 @@ def test_refusals(cuda_device):
     with pytest.raises(ripe.RipeError) as e:
         p.gpu.verify_attn(0, 0, odd)
     assert e.value.status == ripe.RIPE_EINVAL
+    p.gpu.set_scores(1e-39)  # 2 log2(e) / cap = 2.9e39 is above the largest fp32, 3.4e38
+    for scale in (1.0, float("nan"), float("inf")):
+        with pytest.raises(ripe.RipeError) as e:
+            p.gpu.verify_attn(0, 0, q, scale=scale)
+        assert e.value.status == ripe.RIPE_EINVAL
     p.close()
