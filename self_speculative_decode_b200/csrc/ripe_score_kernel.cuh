@@ -84,7 +84,7 @@ struct SCfg {
     static constexpr int MERGE_FLOATS = SLOTS * NQ * DP;
     // WIDE: column maxima and l_fix of each warp, references of each group
     static constexpr int GM_FLOATS = WIDE ? (2 * NCW + TG) * NQ : 0;
-    static constexpr int MLF = NCW * NQ * 4 + ROWS * (NPF + 4) + 3 * ROWS + GM_FLOATS + (WIDE ? 4 * TG : 0);
+    static constexpr int MLF = NCW * NQ * 4 + ROWS * (NPF + 4) + 3 * ROWS + 4 * ROWS + GM_FLOATS + (WIDE ? 4 * TG : 0);
     static_assert(MLF % 4 == 0 && (ROWS * NPF) % 4 == 0, "alignment");
     static constexpr int MISC = 1024 + 1024;
     static constexpr int AVAIL =
@@ -192,21 +192,20 @@ struct ScoreChunk {
 
 // Tiles that begin before offset g of the line (with `upto`: at or before it); the pair of the tile that comes next
 // (upto: of the last of them), and its index.
-__device__ __forceinline__ int score_tiles_before(const ScoreArgs &a, const int *cum, const int *real, const int *Ts, int kvH,
-                                                  int g, bool upto, int &pair, int &lt) {
+__device__ __forceinline__ int3 score_tiles_before(const ScoreArgs &a, const int *cum, const int *real, const int *Ts, int kvH,
+                                                int g, bool upto) {
     const int n = seq_of(cum, a.N, g);
     const ScoreGeom sg = score_geom(Ts[n], a.plan);
     const int kh = (g - cum[n]) / sg.cost, off = g - cum[n] - kh * sg.cost;
-    lt = score_first(sg, off + (upto ? 1 : 0), a.plan);
+    int lt = score_first(sg, off + (upto ? 1 : 0), a.plan), pair = n * kvH + kh;
     const int before = real[n] + kh * sg.total + lt;
-    pair = n * kvH + kh;
     if (upto) {
         if (--lt < 0) --pair;  // the last tile is the previous head's
     } else if (lt == sg.total) {
         lt = 0;  // the rest of the head's cost holds no tile; kh + 1 == kvH is the next sequence's first head
         ++pair;
     }
-    return before;
+    return make_int3(before, pair, lt);
 }
 
 // The CTAs that hold tiles of a pair: the first of them, and how many.
@@ -220,28 +219,22 @@ __device__ __forceinline__ int2 score_parts(const ScoreArgs &a, const ScoreChunk
     return make_int2(first, (start + last) / c.chunk - first + 1);
 }
 
-// Chunks of `chunk` costs, or, where all heads cost the same (cost0) and there are fewer heads than CTAs, `pieces`
+// Chunks of `chunk` costs, or, where all heads cost the same (cost0) and there are no more of them than CTAs, `pieces`
 // equal pieces of every head.  A head that a CTA shares costs it head_cost once more, so that pieces, which share
-// nothing across heads, are taken when they are no longer than a chunk (their own head_cost left out), and chunks
-// end on heads when that lengthens them by at most head_cost.
-__device__ __forceinline__ void score_cut(const ScoreArgs &a, int total, int cost0, bool same, int kvH, int &chunk,
-                                          int &pieces) {
-    const int grid = static_cast<int>(gridDim.x), head = a.plan.head_cost;
-    chunk = max(cdiv(total, grid), a.min_chunk);
-    pieces = 0;
-    if (!same) return;
-    if (chunk < cost0) {
-        const int P = min(grid / (a.N * kvH), cost0 / a.min_chunk);
-        if (P < 1) return;
+// nothing across heads, are taken when they are no longer than a chunk (their own head_cost left out) or short
+// anyway; with more heads, chunks end on heads when that lengthens them by at most head_cost.
+__device__ __forceinline__ int2 score_cut(const ScoreArgs &a, int total, int cost0, bool same, int kvH) {
+    const int grid = static_cast<int>(gridDim.x), head = a.plan.head_cost, heads = a.N * kvH;
+    int chunk = max(cdiv(total, grid), a.min_chunk);
+    if (same && heads <= grid) {
+        const int P = min(grid / heads, max((cost0 - head) / a.min_chunk, 1));
         const int piece = max(cdiv(cost0 - head, P), a.plan.ring_cost);  // no shorter than a tile: each holds one
-        if (piece <= chunk) {
-            chunk = piece;
-            pieces = P;
-        }
-    } else {
+        if (piece <= max(chunk, a.min_chunk + head)) return make_int2(piece, P);
+    } else if (same && chunk >= cost0) {
         const int whole = cdiv(chunk, cost0) * cost0;
         if (whole <= chunk + head) chunk = whole;
     }
+    return make_int2(chunk, 0);
 }
 
 __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum, int *real, int *Ts, int *sflag, int tid,
@@ -258,7 +251,9 @@ __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum,
             cum[1] = sg.cost * kvH;
             real[0] = 0;
         }
-        score_cut(a, sg.cost * kvH, sg.cost, true, kvH, c.chunk, c.pieces);
+        const int2 cut = score_cut(a, sg.cost * kvH, sg.cost, true, kvH);
+        c.chunk = cut.x;
+        c.pieces = cut.y;
         __syncthreads();
         pdl_trigger();  // the next kernel may be scheduled; it waits for this one to finish
         if (c.pieces) {
@@ -305,10 +300,9 @@ __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum,
                 rcarry += __shfl_sync(0xffffffffu, r, 31);
             }
             if (lane == 0) {
-                int ch, pc;
-                score_cut(a, carry, first / kvH, same, kvH, ch, pc);
-                sflag[6] = ch;
-                sflag[7] = pc;
+                const int2 cut = score_cut(a, carry, first / kvH, same, kvH);
+                sflag[6] = cut.x;
+                sflag[7] = cut.y;
             }
         }
         __syncthreads();
@@ -326,9 +320,19 @@ __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum,
     }
     const int begin = blockIdx.x * c.chunk, end = min(cum[N], begin + c.chunk);
     if (begin >= end) return c;
-    int lt_end;
-    const int before = score_tiles_before(a, cum, real, Ts, kvH, begin, false, c.p_first, c.lt);
-    c.ntiles = score_tiles_before(a, cum, real, Ts, kvH, end - 1, true, c.p_last, lt_end) - before;
+    int before = 0;
+#pragma unroll 1  // one copy of the code: a small launch is paced by fetching instructions
+    for (int k = 0; k < 2; ++k) {
+        const int3 at = score_tiles_before(a, cum, real, Ts, kvH, k ? end - 1 : begin, k);
+        if (k == 0) {
+            before = at.x;
+            c.p_first = at.y;
+            c.lt = at.z;
+        } else {
+            c.ntiles = at.x - before;
+            c.p_last = at.y;
+        }
+    }
     return c;
 }
 
@@ -350,7 +354,8 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     float *qscale = fin + C::ROWS * 4;                                    // [ROWS] sx over the row's power of two
     float *qslope = qscale + C::ROWS;                                     // [ROWS] distance bias of the row's head
     int *qpos = reinterpret_cast<int *>(qslope + C::ROWS);                // [ROWS] block position, -1: no such row
-    float *gmax = reinterpret_cast<float *>(qpos + C::ROWS);              // WIDE [NCW][NQ] column maxima
+    int4 *qsees = reinterpret_cast<int4 *>(qpos + C::ROWS);               // [ROWS] keys a row sees (stage_q)
+    float *gmax = reinterpret_cast<float *>(qsees + C::ROWS);             // WIDE [NCW][NQ] column maxima
     float *gfix = gmax + C::NCW * C::NQ;                                  // WIDE [NCW][NQ] l_fix
     float *gref = gfix + C::NCW * C::NQ;                                  // WIDE [TG][NQ] m_ref
     // WIDE [TG][4]: the last even and the last odd block that moves a reference; the group has given up; -
@@ -550,16 +555,27 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         }
     };
     auto stage_q = [&](int p) {
-        const int h = head_of(p), row0 = group_row(p), mq = rows_of(p);
+        if (tid < C::ROWS) {  // a thread for each row's position, bias and visible keys
+            const int h = head_of(p), row = group_row(p) + tid, j = row / a.g;
+            const bool have = tid < rows_of(p);
+            // keys [x, y) of RING tiles at plane w, keys [0, z) of DUAL tiles; of other tiles, keys before T
+            int4 r = make_int4(0, 0, 0, -1);
+            if (have) {
+                int lo;
+                const int T = Ts[p / kvH], lq = pa.jloop[pa.j0 + j];
+                score_range(pa, T, kDual, pa.R - 1, pa.j0 + j, lq, lo, r.z);
+                score_range(pa, T, kRing, lq, pa.j0 + j, lq, r.x, r.y);
+                r.w = lq;
+            }
+            qsees[tid] = r;
+            qpos[tid] = have ? pa.j0 + j : -1;
+            if (MOD)
+                qslope[tid] = a.slopes && have ? __ldg(a.slopes + h * a.g + row - j * a.g) * 1.4426950408889634f : 0.f;
+        }
 #pragma unroll
         for (int r = 0; r < QR; ++r) {
             const int i = warp + r * C::NCW;
             if (i >= C::ROWS) break;
-            const bool have = i < mq;
-            const int row = row0 + i, j = have ? row / a.g : 0, hg = have ? row - j * a.g : 0;
-            if (lane == 0) qpos[i] = have ? pa.j0 + j : -1;
-            if (MOD && lane == 0)
-                qslope[i] = a.slopes && have ? __ldg(a.slopes + h * a.g + hg) * 1.4426950408889634f : 0.f;
             float up = 1.f;
             if constexpr (Q8) {
                 uint32_t most = 0;  // largest magnitude of the row, as bf16 bits
@@ -889,8 +905,14 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                 const float slope = MOD ? qslope[col] : 0.f;
                 const float dist = MOD ? static_cast<float>(first - (dsc.T + jq)) : 0.f;
                 int lo = 0, hi = 0, sink = 0, win = 0;
-                if (!FAST && jq >= 0) {
-                    score_range(pa, dsc.T, dsc.kind, dsc.plane, jq, pa.jloop[jq], lo, hi);
+                if (!FAST) {
+                    const int4 r = qsees[col];
+                    if (dsc.kind == kRing) {
+                        lo = r.x;
+                        hi = r.w == dsc.plane ? r.y : 0;
+                    } else {
+                        hi = dsc.kind == kDual ? r.z : dsc.T;
+                    }
                     hi = min(hi, t0 + cnt) - first;
                     lo -= first;
                     if (pa.dwin >= 0) {
@@ -1258,11 +1280,12 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
     if (a.early) pdl_wait();  // the caller may be writing the queries
     fetch_q(P_first);
     if (tid == 32) {
-        const int2 f = score_parts(a, cp, cum, Ts, kvH, P_first), l = score_parts(a, cp, cum, Ts, kvH, P_last);
-        sflag[8] = f.x;
-        sflag[9] = f.y;
-        sflag[10] = l.x;
-        sflag[11] = l.y;
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            const int2 f = score_parts(a, cp, cum, Ts, kvH, k ? P_last : P_first);
+            sflag[8 + 2 * k] = f.x;
+            sflag[9 + 2 * k] = f.y;
+        }
     }
     for (int p = P_first; p <= P_last; ++p) {
         reset_state();
