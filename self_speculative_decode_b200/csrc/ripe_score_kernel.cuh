@@ -29,6 +29,11 @@
 //   * tanh y = 1 - 2 / (1 + e^2y): one exponential and one reciprocal, absolute error 2^-22 of the cap
 //     (the hardware's tanh is 2^-11 relative: 0.02 at a cap of 50).
 //   * A masked value never reaches a sum: stale ring rows or later draft rows may hold NaN or infinity.
+//
+// Measured (one B200, 8 sequences x 32768 keys, 8 kv heads x 128; 6456 GB/s is the measured copy): over the 8-bit
+// region 88 us at 4 rows a kv head (0.94 of it), 102 us at 16 (0.82), 160 to 166 us at 32 (0.50 to 0.52: paced by instructions, 3.25 warps a
+// scheduler; 178 us with 16 rows and 32 keys a warp, 180 us with 32 rows, 16 keys and all of head_dim a warp, 194 us with
+// two groups instead of three); capped, over bf16, 193 to 200 us at 32 rows (0.83 to 0.86).
 #pragma once
 
 #include <cuda_fp16.h>
