@@ -5,8 +5,9 @@
 // the ring holds until then: the region's contents depend on the committed positions alone, not on how
 // they were split into draft blocks.  Bytes moved bound these kernels (256 d bf16 in, 128 d out per
 // block); eviction finds a whole block in one commit of 64 accepted tokens per sequence and head.
-// Measured: the prefix of 8 sequences x 32768 positions, 8 heads x 128, with the ring's share 350 us (4.6 TB/s);
-// dividing every element and storing bytes took 580 us.
+// Measured: the prefix of 8 sequences x 32768 positions, 8 heads x 128, with the ring's share 333 us (4.8 TB/s);
+// dividing every element and storing bytes took 580 us, four CTAs an SM instead of five 350 us.  A commit that evicts
+// a block from each of 14080 heads x 96 178 us (2.9 TB/s), with three CTAs an SM 195 us.
 #include "ripe_score.cuh"
 
 namespace ripe {
@@ -143,7 +144,7 @@ __device__ __forceinline__ void quantise_block(const uint4 *__restrict__ k, cons
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 5)
 ripe_q8_load_kernel(uint8_t *__restrict__ rec, const uint4 *__restrict__ k, const uint4 *__restrict__ v,
                     const HostIntArray T, int N, int kvH, int rec_blocks, int W, int layer, int most_blocks,
                     long long ld_t) {
@@ -187,7 +188,7 @@ __global__ void ripe_q8_load_ring_kernel(uint4 *__restrict__ Kw, uint4 *__restri
 // At a commit: the block whose last position leaves the window, if any (an accepted length of at most 64
 // completes at most one), from ring plane R-1.
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 ripe_q8_evict_kernel(uint8_t *__restrict__ rec, const uint4 *__restrict__ Kw, const uint4 *__restrict__ Vw,
                      const int32_t *__restrict__ T, const HostIntArray acc_h, const int32_t *acc_d, int L, int N,
                      int B, int kvH, int R, int S, int W, int rec_blocks) {
