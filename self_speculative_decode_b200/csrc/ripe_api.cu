@@ -264,7 +264,15 @@ int ripe_set_scores(ripe_cache_t *c, float softcap, const float *slopes, void *s
     if (capture != cudaStreamCaptureStatusNone) return RIPE_ESTATE;
     if (ensure_score_attributes(c->device) != RIPE_OK) return RIPE_ECUDA;
     if (slopes) {
-        if (!c->slopes_dev && !dalloc(&c->slopes_dev, c->Hq * sizeof(float), &c->scratch_bytes)) return RIPE_ENOMEM;
+        if (!c->slopes_dev) {  // not dalloc: its memset runs on the legacy stream, in no order with the copy on s
+            void *p = nullptr;
+            if (cudaMalloc(&p, c->Hq * sizeof(float)) != cudaSuccess) {
+                cudaGetLastError();
+                return RIPE_ENOMEM;
+            }
+            c->slopes_dev = static_cast<float *>(p);
+            c->scratch_bytes += c->Hq * sizeof(float);
+        }
         // attention launches on the stream may still read the old slopes; the caller's array is read by the
         // time the call returns, pinned or not
         if (cudaMemcpyAsync(c->slopes_dev, slopes, c->Hq * sizeof(float), cudaMemcpyHostToDevice, s) != cudaSuccess ||
