@@ -65,7 +65,9 @@ enum ripe_window_mode { RIPE_WINDOW_QUERY_RELATIVE = 0, RIPE_WINDOW_CACHE_RELATI
 /* Device error bits reported by ripe_get_device_error(). */
 enum ripe_device_error {
     RIPE_DEVERR_WAIT_TIMEOUT = 1u, /* a kernel gave up waiting for its own copies */
-    RIPE_DEVERR_CAPACITY = 2u,     /* a kernel saw T + B > max_T and skipped its work */
+    RIPE_DEVERR_CAPACITY = 2u,     /* a kernel saw T + B > max_T and skipped its work: the block's rows are not
+                                      written, the outputs of its queries mean nothing, and a commit accepts
+                                      none of it (a captured step replayed past the capacity; T_n stays) */
     RIPE_DEVERR_ACCEPT = 4u,       /* a device-side accepted length was outside [0, B] */
     RIPE_DEVERR_BOUNDS = 8u        /* debug builds: a tile, slot or scratch index fell outside its
                                       region (the access is still made in bounds: TMA clips it) */

@@ -399,6 +399,23 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Accepted length of a sequence at a commit, from the host (kernel parameter) or from device memory.  A block that
+// did not fit (T + B > max_T, which the host cannot see when a captured step is replayed) was never written: nothing
+// of it is accepted, and T never passes max_T.  err, unless null, receives the error bits.
+__device__ __forceinline__ int accepted(const HostIntArray &ah, const int32_t *ad, int n, int B, int T, int max_T,
+                                        uint32_t *err) {
+    int a = ad ? ad[n] : ah.v[n];
+    if (T + B > max_T) {
+        if (err) atomicOr(err, RIPE_DEVERR_CAPACITY);
+        return 0;
+    }
+    if (a < 0 || a > B) {
+        if (err) atomicOr(err, RIPE_DEVERR_ACCEPT);
+        a = a < 0 ? 0 : B;
+    }
+    return a;
+}
+
 __device__ __forceinline__ void named_bar_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }

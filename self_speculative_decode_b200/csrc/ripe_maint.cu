@@ -73,16 +73,6 @@ int launch_append(ripe_cache *c, int layer, int r, int B, const void *k, const v
 }
 
 // ---------------------------------------------------------------- commit / evict
-// Accepted length of sequence n: from the host (kernel parameter) or from device memory.
-__device__ __forceinline__ int accepted(const HostIntArray &ah, const int32_t *ad, int n, int B,
-                                        uint32_t *err, bool report) {
-    int a = ad ? ad[n] : ah.v[n];
-    if (a < 0 || a > B) {
-        if (report) atomicOr(err, RIPE_DEVERR_ACCEPT);
-        a = a < 0 ? 0 : B;
-    }
-    return a;
-}
 
 // Positions [max(0, T - W), max(0, T + a - W)) leave the window: their deepest plane moves
 // from the ring to the deepest-plane region; planes 0..R-2 are dropped (their slots are
@@ -91,13 +81,13 @@ __global__ void ripe_evict_kernel(uint4 *__restrict__ Kd, uint4 *__restrict__ Vd
                                   const uint4 *__restrict__ Kw, const uint4 *__restrict__ Vw,
                                   const int32_t *__restrict__ T, const HostIntArray acc_h,
                                   const int32_t *acc_d, uint32_t *err, int N, int B, int kvH, int d8,
-                                  int R, int S, int W, int deep_rows) {
+                                  int R, int S, int W, int deep_rows, int max_T) {
     pdl_wait();
     pdl_trigger();
     const int layer = blockIdx.x / N;
     const int n = blockIdx.x - layer * N;
     const int Tn = T[n];
-    const int a = accepted(acc_h, acc_d, n, B, err, false);
+    const int a = accepted(acc_h, acc_d, n, B, Tn, max_T, nullptr);
     const int lo = Tn - W > 0 ? Tn - W : 0;
     const int hi = Tn + a - W > 0 ? Tn + a - W : 0;
     const int npos = hi - lo;
@@ -119,10 +109,10 @@ __global__ void ripe_evict_kernel(uint4 *__restrict__ Kd, uint4 *__restrict__ Vd
 }
 
 __global__ void ripe_commit_lengths_kernel(int32_t *T, const HostIntArray acc_h, const int32_t *acc_d,
-                                           uint32_t *err, int N, int B) {
+                                           uint32_t *err, int N, int B, int max_T) {
     pdl_wait();
     pdl_trigger();
-    for (int n = threadIdx.x; n < N; n += blockDim.x) T[n] += accepted(acc_h, acc_d, n, B, err, true);
+    for (int n = threadIdx.x; n < N; n += blockDim.x) T[n] += accepted(acc_h, acc_d, n, B, T[n], max_T, err);
 }
 
 int launch_commit(ripe_cache *c, const int32_t *acc_host, const int32_t *acc_dev, cudaStream_t s) {
@@ -141,12 +131,13 @@ int launch_commit(ripe_cache *c, const int32_t *acc_host, const int32_t *acc_dev
         launch_pdl(ripe_evict_kernel, grid, dim3(256), 0, s, reinterpret_cast<uint4 *>(c->Kd),
                    reinterpret_cast<uint4 *>(c->Vd), reinterpret_cast<const uint4 *>(c->Kw),
                    reinterpret_cast<const uint4 *>(c->Vw), static_cast<const int32_t *>(c->T_dev), ah, acc_dev,
-                   c->err_dev, c->N, c->B_cur, c->kvH, d8, c->R, c->ring_slots, c->W, c->deep_rows);
+                   c->err_dev, c->N, c->B_cur, c->kvH, d8, c->R, c->ring_slots, c->W, c->deep_rows,
+                   c->max_T);
         c->launches += 1;
         if (cudaGetLastError() != cudaSuccess) return RIPE_ECUDA;
     }
     launch_pdl(ripe_commit_lengths_kernel, dim3(1), dim3(256), 0, s, c->T_dev, ah, acc_dev, c->err_dev, c->N,
-               c->B_cur);
+               c->B_cur, c->max_T);
     c->launches += 1;
     c->lengths_dirty = true;
     if (cudaGetLastError() != cudaSuccess) return RIPE_ECUDA;

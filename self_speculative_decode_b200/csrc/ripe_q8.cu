@@ -191,7 +191,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 4)
 ripe_q8_evict_kernel(uint8_t *__restrict__ rec, const uint4 *__restrict__ Kw, const uint4 *__restrict__ Vw,
                      const int32_t *__restrict__ T, const HostIntArray acc_h, const int32_t *acc_d, int L, int N,
-                     int B, int kvH, int R, int S, int W, int rec_blocks) {
+                     int B, int kvH, int R, int S, int W, int rec_blocks, int max_T) {
     __shared__ __align__(16) uint8_t buf[128 * D];
     __shared__ uint32_t red[16];
     pdl_wait();
@@ -199,8 +199,7 @@ ripe_q8_evict_kernel(uint8_t *__restrict__ rec, const uint4 *__restrict__ Kw, co
     const int items = L * N * kvH;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
         const int kh = it % kvH, n = (it / kvH) % N, layer = it / kvH / N;
-        int a = acc_d ? acc_d[n] : acc_h.v[n];
-        a = a < 0 ? 0 : a > B ? B : a;  // the length update reports values outside [0, B]
+        const int a = accepted(acc_h, acc_d, n, B, T[n], max_T, nullptr);  // (the length update reports)
         const int p0 = q8_end(T[n], W);
         if (q8_end(T[n] + a, W) == p0 || p0 / kQ8Block >= rec_blocks) continue;
         const size_t row0 = ring_row(layer, n, R - 1, kh, 0, N, R, kvH, S);
@@ -351,7 +350,7 @@ int launch_q8_evict(ripe_cache *c, const HostIntArray &acc_host, const int32_t *
         launch_pdl(ripe_q8_evict_kernel<decltype(d)::value>, dim3(grid), dim3(kThreads), 0, s, c->rec8,
                    reinterpret_cast<const uint4 *>(c->Kw), reinterpret_cast<const uint4 *>(c->Vw),
                    static_cast<const int32_t *>(c->T_dev), acc_host, acc_dev, c->L, c->N, c->B_cur, c->kvH, c->R,
-                   c->ring_slots, c->W, c->rec_blocks);
+                   c->ring_slots, c->W, c->rec_blocks, c->max_T);
     });
 }
 

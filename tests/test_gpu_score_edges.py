@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from self_speculative_decode_b200 import ripe
 from score_ref import Pair, bits_dev
 
 pytestmark = pytest.mark.gpu
@@ -28,4 +29,43 @@ def test_first_slopes_set_on_a_side_stream(cuda_device, bits):
     p.gpu.verify_attn(0, 0, qd, out=out, lse=lse, stream=s)
     s.synchronize()
     p.check(out, lse, q, 0)
+    p.close()
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+def test_a_step_replayed_past_the_capacity(cuda_device, bits):
+    """A captured step knows no host lengths: a block that no longer fits is reported, none of it is accepted, and the
+    lengths stay within the cache, whose other sequence and earlier positions are as they should be."""
+    p = Pair(2, 4, 2, 64, 2, 8, [50, 150], 4, bits=bits, cap=20.0, room=6, seed=18).load()
+    kv = [[torch.empty((2, 4, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)] for _ in range(2)]
+    q = torch.empty((2, 4, 4, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(q), p.lse(4)
+    acc = torch.full((2,), 4, dtype=torch.int32, device="cuda")
+
+    def step():
+        for r in range(2):
+            p.gpu.append_block(0, r, *kv[r])
+        p.gpu.verify_attn(0, 0, q, out=out, lse=lse)
+        p.gpu.commit_device(acc)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(5):  # 150 -> 154 -> 158, and 158 + 4 > 160
+        T = list(p.T)
+        p.T = [min(t, p.max_T - 4) for t in T]
+        qb = p.queries(4)
+        q.copy_(bits_dev(qb))
+        for r in range(2):
+            for dst, src in zip(kv[r], p.rows(0, r, 0, 4)):
+                dst.copy_(bits_dev(src))
+        p.T = T
+        g.replay()
+        torch.cuda.synchronize()
+        p.check(out, lse, qb, 0, rows={(0, j) for j in range(4)} | ({(1, j) for j in range(4)} if i < 2 else set()))
+        p.T = [T[0] + 4, T[1] + (4 if i < 2 else 0)]
+    assert p.gpu.device_error() == ripe.RIPE_DEVERR_CAPACITY
+    assert p.gpu.sync_lengths() == p.T == [70, 158]
+    p.append(2).verify(0, 2)
+    p.verify(1, 2)
     p.close()
