@@ -423,6 +423,8 @@ __device__ __forceinline__ void named_bar_sync(int id, int threads) {
 
 // Launch with programmatic stream serialization: the kernel may start while the previous one
 // drains; every such kernel calls pdl_wait() before touching memory a previous kernel writes.
+// What it reads of that afterwards it does not read on the read-only path (__ldg, const __restrict__): that path is
+// for data that nobody writes while the kernel is resident, and the compiler may move its loads up past the wait.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                        Args &&...args) {

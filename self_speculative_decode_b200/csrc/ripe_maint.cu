@@ -45,15 +45,16 @@ __global__ void ripe_append_kernel(uint4 *__restrict__ Kw, uint4 *__restrict__ V
         rest /= kvH;
         const int j = static_cast<int>(rest % B);
         const int n = static_cast<int>(rest / B);
-        const int Tn = T[n];
+        const int Tn = __ldcg(T + n);
         if (Tn + B > max_T) {
             if (j == 0 && kh == 0 && c8 == 0) atomicOr(err, RIPE_DEVERR_CAPACITY);
             continue;
         }
         const int slot = (Tn + j) % S;
         const size_t dst = ring_row(layer, n, r, kh, slot, N, R, kvH, S) * d8 + c8;
-        Kw[dst] = k[idx];
-        Vw[dst] = v[idx];
+        // not the read-only path: a rotation launched before this (ripe_rotate_block) may have been writing them
+        Kw[dst] = __ldcg(k + idx);
+        Vw[dst] = __ldcg(v + idx);
     }
 }
 
@@ -86,7 +87,7 @@ __global__ void ripe_evict_kernel(uint4 *__restrict__ Kd, uint4 *__restrict__ Vd
     pdl_trigger();
     const int layer = blockIdx.x / N;
     const int n = blockIdx.x - layer * N;
-    const int Tn = T[n];
+    const int Tn = __ldcg(T + n);
     const int a = accepted(acc_h, acc_d, n, B, Tn, max_T, nullptr);
     const int lo = Tn - W > 0 ? Tn - W : 0;
     const int hi = Tn + a - W > 0 ? Tn + a - W : 0;
@@ -103,8 +104,8 @@ __global__ void ripe_evict_kernel(uint4 *__restrict__ Kd, uint4 *__restrict__ Vd
         }
         const size_t src = ring_row(layer, n, R - 1, kh, t % S, N, R, kvH, S) * d8 + c8;
         const size_t dst = deep_row(layer, n, kh, t, N, kvH, deep_rows) * d8 + c8;
-        Kd[dst] = Kw[src];
-        Vd[dst] = Vw[src];
+        Kd[dst] = __ldcg(Kw + src);
+        Vd[dst] = __ldcg(Vw + src);
     }
 }
 

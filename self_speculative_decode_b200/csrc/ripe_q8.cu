@@ -67,10 +67,10 @@ __device__ __forceinline__ void quantise_block(const uint4 *__restrict__ k, cons
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = tid + i * kThreads, t = e / D8;
-        xk[i] = k[row(t) * D8 + (e - t * D8)];
+        xk[i] = __ldcg(k + row(t) * D8 + (e - t * D8));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) xv[i] = has_v ? v[row(vt + (i & 1) + 8 * (i >> 1)) * D8 + v8] : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) xv[i] = has_v ? __ldcg(v + row(vt + (i & 1) + 8 * (i >> 1)) * D8 + v8) : make_uint4(0, 0, 0, 0);
     const auto most_of = [](uint32_t m, const uint4 &x) {
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -199,9 +199,9 @@ ripe_q8_evict_kernel(uint8_t *__restrict__ rec, const uint4 *__restrict__ Kw, co
     const int items = L * N * kvH;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
         const int kh = it % kvH, n = (it / kvH) % N, layer = it / kvH / N;
-        const int a = accepted(acc_h, acc_d, n, B, T[n], max_T, nullptr);  // (the length update reports)
-        const int p0 = q8_end(T[n], W);
-        if (q8_end(T[n] + a, W) == p0 || p0 / kQ8Block >= rec_blocks) continue;
+        const int Tn = __ldcg(T + n), p0 = q8_end(Tn, W);
+        const int a = accepted(acc_h, acc_d, n, B, Tn, max_T, nullptr);  // (the length update reports)
+        if (q8_end(Tn + a, W) == p0 || p0 / kQ8Block >= rec_blocks) continue;
         const size_t row0 = ring_row(layer, n, R - 1, kh, 0, N, R, kvH, S);
         quantise_block<D>(Kw, Vw, [&](int t) { return row0 + (p0 + t) % S; },
                           rec + (static_cast<size_t>(it) * rec_blocks + p0 / kQ8Block) * q8_record_bytes(D), buf, red);

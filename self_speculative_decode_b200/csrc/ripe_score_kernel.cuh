@@ -542,8 +542,8 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
 
     // All consumer warps: Q of pair p into shared memory, in fragment order.  bf16: of each 16 columns, lane
     // (g4, c4) has 2 c4, 2 c4 + 1 and 8 more; f16: 4 c4 .. 4 c4 + 3, the order of the 8-bit K fragments.
-    // fetch_q starts the loads (a warp has rows warp, warp + NCW, ..; all of them in flight together), stage_q
-    // writes the rows.
+    // fetch_q starts the loads (a warp has rows warp, warp + NCW, ..; all of them in flight together; not on the
+    // read-only path, as ripe_verify.cu), stage_q writes the rows.
     constexpr int QW = (D + 63) / 64, QR = (C::ROWS + C::NCW - 1) / C::NCW;
     uint32_t qw[QR][QW];
     auto fetch_q = [&](int p) {
@@ -556,7 +556,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             const uint32_t *qp = reinterpret_cast<const uint32_t *>(
                 a.q + ((static_cast<size_t>(p / kvH) * a.qB + j) * a.Hq + h * a.g + hg) * D);
 #pragma unroll
-            for (int u = 0; u < QW; ++u) qw[r][u] = have && u * 32 + lane < D / 2 ? __ldg(qp + u * 32 + lane) : 0u;
+            for (int u = 0; u < QW; ++u) qw[r][u] = have && u * 32 + lane < D / 2 ? __ldcg(qp + u * 32 + lane) : 0u;
         }
     };
     auto stage_q = [&](int p) {

@@ -69,3 +69,38 @@ def test_a_step_replayed_past_the_capacity(cuda_device, bits):
     p.append(2).verify(0, 2)
     p.verify(1, 2)
     p.close()
+
+
+@pytest.mark.parametrize("bits,Hq,B", [(16, 6, 5), (16, 6, 8), (8, 6, 5), (8, 6, 8)])
+def test_calls_behind_a_rotation_in_place_read_what_it_wrote(cuda_device, bits, Hq, B):
+    """Rotation, append and verification of several steps queued without a pause give what they give one at a time."""
+    N, kvH, d, W = 9, 2, 96, 16
+    c = ripe.RipeCache(N, 1, Hq, kvH, d, 2, W, 400, B, kv_bits=bits)
+    kv = torch.randn((N, kvH, 300, d), device="cuda").bfloat16()
+    for r in range(2):
+        c.load_prefix(0, r, [300 - 20 * n for n in range(N)], kv, kv)
+    angle = torch.arange(400, device="cuda")[:, None] * 0.01 ** (torch.arange(48, device="cuda") / 48)
+    t = ripe.RotaryTable(angle.cos(), angle.sin())
+    steps = [[torch.randn((N, B, h, d), device="cuda").bfloat16() for h in (Hq, kvH, kvH)] for _ in range(30)]
+
+    def run(pause):
+        out = []
+        for i, (q, k, v) in enumerate(steps):
+            q, k = q.clone(), k.clone()
+            pause()
+            if i % 2:
+                c.append_block_rope(0, 0, k, v, t, q, q_out=q)
+            else:
+                c.rotate_block(0, t, k, q, k_out=k, q_out=q)
+                pause()
+                c.append_block(0, 0, k, v)
+            pause()
+            out.append(c.verify_attn(0, 0, q))
+        return out
+
+    run(lambda: None)
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
+    assert c.device_error() == 0
+    c.close()
