@@ -717,11 +717,9 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < C::NPF; ++w) {
-                const float f = wq[i * C::NPF + w];
-                if (f != 0.f) {
-                    const float4 v = *reinterpret_cast<const float4 *>(&mo[((w * WR + rgi) * C::NQ + q) * C::DP + c0]);
-                    acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
-                }
+                const float f = wq[i * C::NPF + w];  // 0 too: what a weight of 0 does to a NaN stays a NaN
+                const float4 v = *reinterpret_cast<const float4 *>(&mo[((w * WR + rgi) * C::NQ + q) * C::DP + c0]);
+                acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
             }
             if (sole) {
                 write_row(p, i, c0, acc, fin[i * 4], fin[i * 4 + 1], fin[i * 4 + 2]);
@@ -763,12 +761,13 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                 float L = 0.f, Ll = 0.f;
 #pragma unroll
                 for (int c = 0; c < FEW; ++c) {
-                    const float w = c >= nparts || ml[c].x == -INFINITY ? 0.f : exp2f(ml[c].x - M);
-                    if (w != 0.f) {
-                        acc.x += w * v[c].x; acc.y += w * v[c].y; acc.z += w * v[c].z; acc.w += w * v[c].w;
-                        L += w * ml[c].y;
-                        Ll += w * ml[c].z;
-                    }
+                    if (c >= nparts) continue;
+                    // a partial of weight 0 is added all the same: one that has seen a NaN alone has no maximum, and
+                    // its NaN has to reach the row
+                    const float w = ml[c].x == -INFINITY ? 0.f : exp2f(ml[c].x - M);
+                    acc.x += w * v[c].x; acc.y += w * v[c].y; acc.z += w * v[c].z; acc.w += w * v[c].w;
+                    L += w * ml[c].y;
+                    Ll += w * ml[c].z;
                 }
                 write_row(p, i, 4 * cx, acc, M, L, Ll);
             }

@@ -104,3 +104,41 @@ def test_calls_behind_a_rotation_in_place_read_what_it_wrote(cuda_device, bits, 
         assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
     assert c.device_error() == 0
     c.close()
+
+
+# ------------------------------------------------------------------ NaN in one part of a split head
+# 1 head, 700 keys: the list of tiles is cut into two to four pieces, the first of which hold nothing but NaN.  Query rows
+# 2..64 cover the kernel's shapes; with q_std 60 the other keys' maximum lies above 2^126 times the first pieces'
+# reference.
+@pytest.mark.parametrize("q_std,nan", [(1.0, 128), (1.0, 256), (1.0, 384), (60.0, 256), (60.0, 448)])
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("w", [0, 1])
+@pytest.mark.parametrize("Hq,B", [(2, 1), (4, 4), (8, 3), (8, 4), (8, 8)])
+def test_a_part_of_a_head_that_is_all_nan(cuda_device, q_std, nan, bits, w, Hq, B):
+    p = Pair(1, Hq, 1, 64, 1, 8, 700, B, bits=bits, cap=1000.0 if bits == 16 else 0.0, seed=3, q_std=q_std)
+    p.planes[0][0][w][0, :, :nan] = 0x7FC0
+    p.load().append(B)
+    lse = p.lse(B)
+    out = p.gpu.verify_attn(0, 0, bits_dev(p.queries(B)), lse=lse)
+    assert out.isnan().all()
+    if w == 0:
+        assert lse.isnan().all()
+    elif bits == 16:  # a value moves no score
+        assert lse.isfinite().all()
+    p.close()
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("T", [20, 700, 3000])
+@pytest.mark.parametrize("Hq,B", [(2, 1), (4, 4), (8, 3), (8, 8)])
+def test_a_query_with_nan_has_a_nan_log_sum_exp(cuda_device, bits, T, Hq, B):
+    p = Pair(1, Hq, 1, 64, 1, 8, T, B, bits=bits, cap=25.0, seed=13).load().append(B)
+    qb = p.queries(B)
+    qb[0, B - 1, 1, 3] = 0x7FC0
+    lse = p.lse(B)
+    out = p.gpu.verify_attn(0, 0, bits_dev(qb), lse=lse)
+    bad = torch.zeros((1, B, Hq), dtype=torch.bool, device="cuda")
+    bad[0, B - 1, 1] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert out[~bad].isfinite().all() and lse[~bad].isfinite().all()
+    p.close()
