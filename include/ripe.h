@@ -130,8 +130,8 @@ int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_
  * Device layout: records of 128 d + 32 bytes, (max_T - W) / 64 (rounded down) per (layer, sequence, kv
  * head); ring as for ripe_cache_alloc with S = min(W + max_B + 63, max_T) slots.  stats.deep_rows is the
  * capacity of the 8-bit region in positions.
- * On such a cache ripe_append_verify and the draft calls take two launches, and ripe_verify_attn needs
- * 16-byte aligned q and out (RIPE_EINVAL).
+ * On such a cache ripe_append_verify and the draft calls take two launches, and every attention call needs
+ * 16-byte aligned tensors and a finite scale (RIPE_EINVAL).
  */
 int ripe_cache_alloc_q8(int batch, int layers, int q_heads, int kv_heads, int head_dim, int loops, int window,
                         int max_T, int max_B, int window_mode, ripe_cache_t **out);

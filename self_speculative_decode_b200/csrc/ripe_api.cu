@@ -106,6 +106,11 @@ bool aligned_io(const void *q, const void *out) {
     return ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
 }
 
+// What a call that launch_score serves asks of its arguments; checked before anything of the call is enqueued.
+int check_scored(const ripe_cache *c, const void *q, const void *out, float scale) {
+    return aligned_io(q, out) && std::isfinite(score_factor(c, scale)) ? RIPE_OK : RIPE_EINVAL;
+}
+
 // T_n + j + B positions of every sequence have to fit the cache and the rotation's table
 int check_room(const ripe_cache *c, int j, int B, const ripe_rope *rope) {
     for (int n = 0; n < c->N; ++n)
@@ -377,7 +382,7 @@ int ripe_verify_attn(ripe_cache_t *c, int layer, int r, const void *q, void *out
     const NvtxRange nvtx_range("ripe_verify_attn");
     if (!c || !q || !out || layer < 0 || layer >= c->L || r < 0 || r >= c->R) return RIPE_EINVAL;
     if (c->B_cur == 0 || !c->appended[static_cast<size_t>(layer) * c->R + r]) return RIPE_ESTATE;
-    if (!c->plain() && !aligned_io(q, out)) return RIPE_EINVAL;
+    if (!c->plain() && check_scored(c, q, out, scale) != RIPE_OK) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     if (!c->plain()) {
@@ -396,10 +401,10 @@ int ripe_append_verify(ripe_cache_t *c, int layer, int r, int B, const void *k, 
     if (c->B_cur != 0 && B != c->B_cur) return RIPE_EINVAL;
     for (int n = 0; n < c->N; ++n)
         if (c->T[n] + B > c->max_T) return RIPE_ECAPACITY;
+    if (!c->plain() && (check_scored(c, q, out, scale) != RIPE_OK || !aligned_io(k, v))) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     if (!c->plain()) {
-        if (!aligned_io(q, out) || !aligned_io(k, v)) return RIPE_EINVAL;
         const int64_t ld = static_cast<int64_t>(c->kvH) * c->d;
         int st = launch_append_rope(c, layer, r, 0, B, k, v, ld, nullptr, 0, nullptr, nullptr,
                                     static_cast<cudaStream_t>(stream));
@@ -432,13 +437,13 @@ static int draft_step(ripe_cache_t *c, int layer, int r, int j, int sink, int wi
     if (c->B_cur != 0 || j > c->drafted[idx]) return RIPE_ESTATE;
     for (int n = 0; n < c->N; ++n)
         if (c->T[n] + j + 1 > c->max_T) return RIPE_ECAPACITY;
+    if (!c->plain() && (check_scored(c, q, out, scale) != RIPE_OK || !aligned_io(k, v))) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     int st;
     if (c->plain()) {
         st = launch_draft(c, layer, r, j, k, v, q, out, lse, scale, static_cast<cudaStream_t>(stream), sink, window);
     } else {
-        if (!aligned_io(q, out) || !aligned_io(k, v)) return RIPE_EINVAL;
         st = launch_append_rope(c, layer, r, j, 1, k, v, static_cast<int64_t>(c->kvH) * c->d, nullptr, 0, nullptr,
                                 nullptr, static_cast<cudaStream_t>(stream));
         const ScoreCall call = {layer, r, j + 1, j, 1, sink, window, nullptr, q, out, lse, scale};
@@ -473,7 +478,7 @@ int ripe_verify_attn_wave(ripe_cache_t *c, int layer, const int32_t *loop_of_pos
         if (r < 0 || r >= c->R) return RIPE_EINVAL;
         if (!c->appended[static_cast<size_t>(layer) * c->R + r]) return RIPE_ESTATE;
     }
-    if (!c->plain() && !aligned_io(q, out)) return RIPE_EINVAL;
+    if (!c->plain() && check_scored(c, q, out, scale) != RIPE_OK) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     if (!c->plain()) {

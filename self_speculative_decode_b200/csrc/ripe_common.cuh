@@ -510,6 +510,8 @@ struct ScoreCall {
     float scale;
 };
 int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s);
+// The factor of a call's dot products (ScoreArgs::sx); a call whose factor is not finite is refused.
+float score_factor(const ripe_cache *c, float scale);
 int ensure_score_attributes(int device);  // as ensure_verify_attributes, for launch_score's kernels
 // The 8-bit region (ripe_q8.cu)
 int launch_q8_load_prefix(ripe_cache *c, int layer, int plane, const int32_t *T, const void *k, const void *v,

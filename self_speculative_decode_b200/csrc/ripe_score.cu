@@ -1,10 +1,10 @@
 // Launch of the attention over 8-bit caches or with capped or biased scores, and its instances over bf16
 // caches.
-#include <cmath>
-
 #include "ripe_score_kernel.cuh"
 
 namespace ripe {
+
+constexpr float kLog2e = 1.4426950408889634f;
 
 cudaError_t launch_score_bf16(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s) {
     switch (d) {
@@ -37,6 +37,10 @@ int ensure_score_attributes(int device) {
     }
     done[device] = true;
     return RIPE_OK;
+}
+
+float score_factor(const ripe_cache *c, float scale) {
+    return c->softcap > 0.f ? 2.f * scale * kLog2e / c->softcap : scale * kLog2e;
 }
 
 int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
@@ -94,10 +98,8 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     a.min_chunk = RIPE_MIN_CHUNK;
     a.has_deep = !q8 && c->deep_rows > 0 ? 1 : 0;
     a.early = c->lengths_dirty ? 0 : 1;
-    const float log2e = 1.4426950408889634f;
-    a.cap = c->softcap * log2e;
-    a.sx = c->softcap > 0.f ? 2.f * call.scale * log2e / c->softcap : call.scale * log2e;
-    if (!std::isfinite(a.sx)) return RIPE_EINVAL;  // a scale, or a scale over a cap, that no score survives
+    a.cap = c->softcap * kLog2e;
+    a.sx = score_factor(c, call.scale);  // finite: checked by the caller
     a.dbg_deep_rows = c->deep_rows;
     // partials of two groups of 32 rows take the room of one of 64 (ripe_cache_alloc's scratch)
     a.dbg_part_slots = c->num_sms + c->N * c->kvH * a.groups;

@@ -142,3 +142,33 @@ def test_a_query_with_nan_has_a_nan_log_sum_exp(cuda_device, bits, T, Hq, B):
     assert out[bad].isnan().all() and lse[bad].isnan().all()
     assert out[~bad].isfinite().all() and lse[~bad].isfinite().all()
     p.close()
+
+
+# ------------------------------------------------------------------ refused calls
+@pytest.mark.parametrize("bits,cap", [(8, 0.0), (8, 30.0), (16, 30.0)])
+def test_a_refused_call_leaves_the_cache_as_it_was(cuda_device, bits, cap):
+    """A scale that no score survives is refused before the block's or the draft's rows are written."""
+    p = Pair(2, 4, 2, 64, 2, 8, [100, 200], 3, bits=bits, cap=cap, seed=17).load()
+    junk = torch.full((2, 3, 2, 64), 9.0, dtype=torch.bfloat16, device="cuda")
+    p.draft(0, 0)
+    q1 = bits_dev(p.queries(1))
+    for scale in (float("inf"), float("nan")):
+        with pytest.raises(ripe.RipeError) as e:  # the drafted row again
+            p.gpu.draft_attn(0, 0, 0, junk[:, :1].contiguous(), junk[:, :1].contiguous(), q1, scale=scale)
+        assert e.value.status == ripe.RIPE_EINVAL
+    p.draft(0, 1)  # attends to the row drafted first
+    p.append(3)
+    before = p.gpu.export(0, 0) + p.gpu.export(1, 0)
+    launches = p.gpu.launch_count()
+    q = bits_dev(p.queries(3))
+    for scale in (float("inf"), float("nan")):
+        for call in (lambda: p.gpu.append_verify(0, 1, junk, junk, q, scale=scale),
+                     lambda: p.gpu.verify_attn(0, 1, q, scale=scale),
+                     lambda: p.gpu.verify_attn_wave(0, [0, 1, 0], q, scale=scale)):
+            with pytest.raises(ripe.RipeError) as e:
+                call()
+            assert e.value.status == ripe.RIPE_EINVAL
+    assert p.gpu.launch_count() == launches
+    assert all(torch.equal(a, b) for a, b in zip(before, p.gpu.export(0, 0) + p.gpu.export(1, 0)))
+    p.verify(1, 3)
+    p.close()
