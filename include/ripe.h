@@ -209,14 +209,15 @@ int ripe_rotate_block(ripe_cache_t *c, int j, int B, const void *k, int64_t ld_k
 /*
  * How scores are formed by every later attention call on this cache (verify, wave, draft, windowed
  * draft, append_verify), for models trained with it.  With x = scale * <q, K_plane[t]>:
- *   softcap > 0    x <- softcap * tanh(x / softcap)
+ *   softcap > 0    x <- softcap * tanh(x / softcap), softcap at most 1e36 (RIPE_EINVAL); off by at most
+ *                  2^-21 softcap below 64, and from 64 on by 2^-19 |x|, beside the rounding of x
  *   slopes         host fp32[q_heads] or NULL: x <- x - slopes[h] * (p - t), a bias linear in the
  *                  distance (finite; copied before the call returns; synchronises the stream)
  * softcap 0 and slopes NULL (the state after allocation) give plain scores again.  Not while the
  * stream is captured (RIPE_ESTATE); a captured graph keeps the softcap and the presence of slopes that it
  * was captured with, and reads the slopes of the last call.  With either, the draft calls and
- * ripe_append_verify take two launches, q and out are 16-byte aligned, and scale and scale / softcap are
- * finite (RIPE_EINVAL).
+ * ripe_append_verify take two launches, the tensors of an attention call are 16-byte aligned, and scale * log2(e),
+ * with a softcap below 64 also 2 scale * log2(e) / softcap, is finite in fp32 and softcap not subnormal (RIPE_EINVAL).
  */
 int ripe_set_scores(ripe_cache_t *c, float softcap, const float *slopes, void *stream);
 

@@ -255,7 +255,7 @@ extern "C" {
 
 int ripe_set_scores(ripe_cache_t *c, float softcap, const float *slopes, void *stream) {
     const NvtxRange nvtx_range("ripe_set_scores");
-    if (!c || !(softcap >= 0.f) || std::isinf(softcap)) return RIPE_EINVAL;
+    if (!c || !(softcap >= 0.f) || softcap > kCapMost) return RIPE_EINVAL;
     if (slopes)
         for (int h = 0; h < c->Hq; ++h)
             if (!std::isfinite(slopes[h])) return RIPE_EINVAL;

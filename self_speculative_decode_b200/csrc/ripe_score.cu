@@ -1,5 +1,8 @@
 // Launch of the attention over 8-bit caches or with capped or biased scores, and its instances over bf16
 // caches.
+#include <cfloat>
+#include <cmath>
+
 #include "ripe_score_kernel.cuh"
 
 namespace ripe {
@@ -8,17 +11,17 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 cudaError_t launch_score_bf16(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s) {
     switch (d) {
-        case 64: return ScoreSet<64, false, true>::launch(t, grid, a, s);
-        case 96: return ScoreSet<96, false, true>::launch(t, grid, a, s);
-        case 128: return ScoreSet<128, false, true>::launch(t, grid, a, s);
+        case 64: return ScoreSet<64, false, 1>::launch(t, grid, a, s);
+        case 96: return ScoreSet<96, false, 1>::launch(t, grid, a, s);
+        case 128: return ScoreSet<128, false, 1>::launch(t, grid, a, s);
         default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t set_score_bf16_attributes() {
-    cudaError_t e = ScoreSet<64, false, true>::set_attr();
-    if (e == cudaSuccess) e = ScoreSet<96, false, true>::set_attr();
-    if (e == cudaSuccess) e = ScoreSet<128, false, true>::set_attr();
+    cudaError_t e = ScoreSet<64, false, 1>::set_attr();
+    if (e == cudaSuccess) e = ScoreSet<96, false, 1>::set_attr();
+    if (e == cudaSuccess) e = ScoreSet<128, false, 1>::set_attr();
     return e;
 }
 
@@ -30,7 +33,9 @@ int ensure_score_attributes(int device) {
     if (done[device]) return RIPE_OK;
     cudaError_t e = set_score_q8_attributes();  // the caller makes the device current
     if (e == cudaSuccess) e = set_score_q8_mod_attributes();
+    if (e == cudaSuccess) e = set_score_q8_cap_attributes();
     if (e == cudaSuccess) e = set_score_bf16_attributes();
+    if (e == cudaSuccess) e = set_score_cap_attributes();
     if (e != cudaSuccess) {
         cudaGetLastError();
         return RIPE_ECUDA;
@@ -40,7 +45,8 @@ int ensure_score_attributes(int device) {
 }
 
 float score_factor(const ripe_cache *c, float scale) {
-    return c->softcap > 0.f ? 2.f * scale * kLog2e / c->softcap : scale * kLog2e;
+    if (c->softcap > 0.f && c->softcap < FLT_MIN) return NAN;  // the kernels take subnormals for 0
+    return c->softcap > 0.f && c->softcap < kCapSeries ? 2.f * scale * kLog2e / c->softcap : scale * kLog2e;
 }
 
 int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
@@ -99,6 +105,7 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     a.has_deep = !q8 && c->deep_rows > 0 ? 1 : 0;
     a.early = c->lengths_dirty ? 0 : 1;
     a.cap = c->softcap * kLog2e;
+    a.rcap = c->softcap >= kCapSeries ? 1.f / a.cap : 0.f;
     a.sx = score_factor(c, call.scale);  // finite: checked by the caller
     a.dbg_deep_rows = c->deep_rows;
     // partials of two groups of 32 rows take the room of one of 64 (ripe_cache_alloc's scratch)
@@ -115,7 +122,10 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     if (grid < 1) grid = 1;
     const LaunchTarget t = {&c->tm_Kd, &c->tm_Vd, wide ? &c->tm_Kw32 : &c->tm_Kw, wide ? &c->tm_Vw32 : &c->tm_Vw,
                             c->device, c->num_sms, c->N};
-    const auto launch = !q8 ? launch_score_bf16 : c->scored() ? launch_score_q8_mod : launch_score_q8;
+    const auto launch = a.rcap != 0.f   ? (q8 ? launch_score_q8_cap : launch_score_cap)
+                        : !q8           ? launch_score_bf16
+                        : c->scored()   ? launch_score_q8_mod
+                                        : launch_score_q8;
     const cudaError_t e = launch(c->d, t, grid, a, s);
     c->launches += 1;
     c->lengths_dirty = false;

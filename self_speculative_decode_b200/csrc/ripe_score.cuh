@@ -198,6 +198,10 @@ __host__ __device__ __forceinline__ bool score_sees(const ScorePlan &a, int T, i
 
 // ---------------------------------------------------------------- arguments of one launch
 constexpr int kGroupRows = 32;
+// Caps from here on take `capped` (ripe_score_kernel.cuh): below, the exponential form is off by at most 2^-16 (2^-22
+// of the cap) and faster (8 sequences x 32768 keys, 32 rows: 194 us against 209, in 8 bits 199 against 212).
+constexpr float kCapSeries = 64.f;
+constexpr float kCapMost = 1e36f;   // above it 1 / cap nears the end of fp32
 constexpr int kWideRingRows = 32;  // ring tile of an 8-bit cache with more than 16 rows: as many bytes as a block
 
 struct ScoreArgs {
@@ -215,17 +219,22 @@ struct ScoreArgs {
     int N, kvH, g, Hq, layer, Mq, min_chunk, qB;
     int groups, grows;    // a kv head's Mq query rows in row groups of grows <= kGroupRows
     int has_deep, early;  // as VerifyArgs
-    float sx;             // factor of the dot product: scale * log2(e), or 2 scale log2(e) / cap
+    float sx;             // factor of the dot product: scale * log2(e), or 2 scale log2(e) / cap with a cap below kCapSeries
     float cap;            // cap * log2(e), 0: no cap
+    float rcap;           // 1 / cap for a cap from kCapSeries on, else 0
     int dbg_deep_rows, dbg_part_slots;
     long long dbg_ring_pages;
 };
 
 cudaError_t launch_score_q8(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
 cudaError_t launch_score_q8_mod(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
+cudaError_t launch_score_q8_cap(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
+cudaError_t launch_score_cap(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
 cudaError_t launch_score_bf16(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
 cudaError_t set_score_q8_attributes();
 cudaError_t set_score_q8_mod_attributes();
+cudaError_t set_score_q8_cap_attributes();
+cudaError_t set_score_cap_attributes();
 cudaError_t set_score_bf16_attributes();
 
 }  // namespace ripe

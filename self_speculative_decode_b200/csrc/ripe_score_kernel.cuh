@@ -1,5 +1,5 @@
 // Attention over a RIPE cache whose deepest-plane region is held in 8 bits (Q8), or with capped or
-// distance-biased scores (MOD); included by the translation units that instantiate it.
+// distance-biased scores (MOD; 2: with a cap from kCapSeries on); included by the translation units that instantiate it.
 //
 // What is computed: for every query row of block position p = T + j, over the keys t <= p with the
 // plane rule of ripe_verify_attn,
@@ -27,7 +27,10 @@
 //     m), O sums p' u, and the normaliser sums p' / s.  So a block costs no multiply of its own per
 //     element, and the reference m follows the size of p' u, which is what O accumulates.
 //   * tanh y = 1 - 2 / (1 + e^2y): one exponential and one reciprocal, absolute error 2^-22 of the cap
-//     (the hardware's tanh is 2^-11 relative: 0.02 at a cap of 50).
+//     (the hardware's tanh is 2^-11 relative: 0.02 at a cap of 50).  That error moves the weights as much however
+//     small the scores are, so that caps from kCapSeries on take the odd series where |y| is small (capped): an
+//     error of 2^-19 of the score itself.  They are instances of their own: with both forms in one, capped launches
+//     took up to 4 % longer.
 //   * A masked value never reaches a sum: stale ring rows or later draft rows may hold NaN or infinity.
 //
 // Measured (one B200, 8 sequences x 32768 keys, 8 kv heads x 128; 6456 GB/s is the measured copy): over the 8-bit
@@ -104,6 +107,17 @@ struct SCfg {
     static_assert(MAX_PARTS >= 148, "stage buffers too small for the end-of-CTA merge");
     static constexpr int smem_bytes(int N) { return SMEM_FIXED + (3 * N + 2) * 4; }
 };
+
+// cap tanh(z / cap) for a score z, both in log2 units; rcap = 1 / cap.  Up to |y| = 0.35 the series to y^9 (the next
+// term is 2^-21 of the sum there), beyond it 1 - 2 / (1 + e^2y), whose error of 2^-21.4 (one step of the exponential's and
+// of the reciprocal's 2^-22 each) is 2^-19.8 of tanh 0.35.  A NaN fails the comparison and goes through the exponential.
+__device__ __forceinline__ float capped(float z, float cap, float rcap) {
+    const float y = z * rcap, s = y * y;
+    const float series =
+        fmaf(s, fmaf(s, fmaf(s, fmaf(s, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+    const float far = fmaf(-2.f, __fdividef(1.f, 1.f + exp2f(y * 2.8853900817779268f)), 1.f);
+    return fabsf(y) < 0.35f ? z * series : cap * far;
+}
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -341,7 +355,7 @@ __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum,
     return c;
 }
 
-template <int D, int NQT, int WR, int WK, int TG, bool Q8, bool MOD>
+template <int D, int NQT, int WR, int WK, int TG, bool Q8, int MOD>
 __global__ void __launch_bounds__(SCfg<D, NQT, WR, WK, TG, Q8>::THREADS, 1)
 ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constant__ CUtensorMap tmVd,
                   const __grid_constant__ CUtensorMap tmKw, const __grid_constant__ CUtensorMap tmVw,
@@ -930,7 +944,9 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                     for (int h = 0; h < 2; ++h) {
                         const int kk = 16 * sb + 8 * h;
                         float &v = x[sb][nq][e + 2 * h];
-                        if (MOD && a.cap != 0.f)
+                        if (MOD == 2)
+                            v = capped(v * f, a.cap, a.rcap) + off;
+                        else if (MOD && a.cap != 0.f)
                             v = fmaf(-2.f * a.cap, __fdividef(1.f, 1.f + exp2f(v * f)), a.cap + off);
                         else
                             v = fmaf(v, f, off);
@@ -1362,7 +1378,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
 }
 
 // ---------------------------------------------------------------- host side
-template <int D, int NQT, int WR, int WK, int TG, bool Q8, bool MOD>
+template <int D, int NQT, int WR, int WK, int TG, bool Q8, int MOD>
 struct ScoreInst {
     using C = SCfg<D, NQT, WR, WK, TG, Q8>;
     static constexpr auto kernel = ripe_score_kernel<D, NQT, WR, WK, TG, Q8, MOD>;
@@ -1385,7 +1401,7 @@ struct ScoreInst {
 };
 
 // Query-side configuration by the query rows of a row group.
-template <int D, bool Q8, bool MOD>
+template <int D, bool Q8, int MOD>
 struct ScoreSet {
     using R8 = ScoreInst<D, 1, 1, 4, 2, Q8, MOD>;
     using R16 = ScoreInst<D, 2, 1, 4, 2, Q8, MOD>;

@@ -5,17 +5,17 @@ namespace ripe {
 
 cudaError_t launch_score_q8_mod(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s) {
     switch (d) {
-        case 64: return ScoreSet<64, true, true>::launch(t, grid, a, s);
-        case 96: return ScoreSet<96, true, true>::launch(t, grid, a, s);
-        case 128: return ScoreSet<128, true, true>::launch(t, grid, a, s);
+        case 64: return ScoreSet<64, true, 1>::launch(t, grid, a, s);
+        case 96: return ScoreSet<96, true, 1>::launch(t, grid, a, s);
+        case 128: return ScoreSet<128, true, 1>::launch(t, grid, a, s);
         default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t set_score_q8_mod_attributes() {
-    cudaError_t e = ScoreSet<64, true, true>::set_attr();
-    if (e == cudaSuccess) e = ScoreSet<96, true, true>::set_attr();
-    if (e == cudaSuccess) e = ScoreSet<128, true, true>::set_attr();
+    cudaError_t e = ScoreSet<64, true, 1>::set_attr();
+    if (e == cudaSuccess) e = ScoreSet<96, true, 1>::set_attr();
+    if (e == cudaSuccess) e = ScoreSet<128, true, 1>::set_attr();
     return e;
 }
 

@@ -1,11 +1,55 @@
 """Attention over 8-bit caches and with capped or biased scores at the ends of its range, against 64 bits."""
+import numpy as np
 import pytest
 import torch
 
-from self_speculative_decode_b200 import ripe
-from score_ref import Pair, bits_dev
+from self_speculative_decode_b200 import ripe, synth
+from score_ref import Pair, bits_dev, quantised
 
 pytestmark = pytest.mark.gpu
+
+
+def dense(p, q, n, j, cap=0.0, slopes=None):
+    """out [Hq][d], its tolerance, lse [Hq], its own, of query row q [Hq][d] (bf16 bits) at position T_n + j, over a cache
+    with one plane (R = 1), the deepest one for every key.
+
+    Tolerances as score_ref's: eps is the error of a score, and what the cap adds to it 2^-21 of a cap below 64, 2^-19 of
+    the score from 64 on (csrc/ripe_score_kernel.cuh).  The largest probability is at least 2^7 (the reference moves to
+    2^-7 of the maximum), the smallest f16 step 2^-24: a weight is also off by up to 2^-25 / 2^7 = 2^-32 absolute."""
+    end, D = p.T[n] + j + 1, p.D(n)
+    kv = []
+    for w in range(2):
+        x = synth.bf16_bits_to_f32(p.planes[0][0][w][n][:, :end]).astype(np.float64)
+        if p.bits == 8 and D:
+            u, s = quantised(x[:, :D])
+            x[:, :D] = u.astype(np.float64) * np.repeat(s.astype(np.float64), 64, 1)[:, :, None]
+        kv.append(np.repeat(x, p.g, 0))
+    qf = synth.bf16_bits_to_f32(q).astype(np.float64)
+    x = p.scale * np.einsum("hd,htd->ht", qf, kv[0])
+    eps = p.d * 2.0 ** -23 * abs(p.scale) * np.einsum("hd,htd->ht", abs(qf), abs(kv[0])).max(1)
+    if cap:
+        x = cap * np.tanh(x / cap)
+        eps = eps + (2.0 ** -21 * cap if cap < 64 else 2.0 ** -19 * abs(x).max(1))
+    if slopes is not None:
+        x = x - np.asarray(slopes, np.float64)[:, None] * (end - 1 - np.arange(end))
+    eps = eps + 2.0 ** -21 * abs(x).max(1)
+    m = x.max(1, keepdims=True)
+    w = np.exp(x - m)
+    lse = m[:, 0] + np.log(w.sum(1))
+    w /= w.sum(1, keepdims=True)
+    out = np.einsum("ht,htd->hd", w, kv[1])
+    A, B = np.einsum("ht,htd->hd", w, abs(kv[1] - out[:, None])), np.einsum("ht,htd->hd", w, abs(kv[1]))
+    tol = 2.0 ** -8 * (abs(out) + A) + (2.0 ** -11 + 2 * eps[:, None] + 2.0 ** -18) * B + 2.0 ** -32 * abs(kv[1]).sum(1)
+    return out, tol, lse, eps + 2.0 ** -18 + 2.0 ** -22 * abs(lse)
+
+
+def check(p, out, lse, q, **kw):
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for n in range(p.N):
+        for j in range(q.shape[1]):
+            eo, to, el, tl = dense(p, q[n, j], n, j, **kw)
+            assert (abs(got[n, j] - eo) <= to).all(), (n, j, float((abs(got[n, j] - eo) / to).max()))
+            assert (abs(gl[n, j] - el) <= tl).all(), (n, j, float((abs(gl[n, j] - el) / tl).max()))
 
 
 @pytest.mark.parametrize("bits", [8, 16])
@@ -171,4 +215,42 @@ def test_a_refused_call_leaves_the_cache_as_it_was(cuda_device, bits, cap):
     assert p.gpu.launch_count() == launches
     assert all(torch.equal(a, b) for a, b in zip(before, p.gpu.export(0, 0) + p.gpu.export(1, 0)))
     p.verify(1, 3)
+    p.close()
+
+
+# ------------------------------------------------------------------ caps far above the scores
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("Hq,B", [(2, 1), (4, 4), (8, 4)])
+@pytest.mark.parametrize("cap", [63.0, 64.0, 100.0, 1e3, 1e5, 1e7, 1e12, 1e30, 1e36])
+def test_large_caps(cuda_device, bits, Hq, B, cap):
+    p = Pair(2, Hq, 1, 64, 1, 8, [300, 90], B, bits=bits, seed=23, q_std=8.0).load().append(B)
+    p.gpu.set_scores(cap)
+    qb, lse = p.queries(B), p.lse(B)
+    out = p.gpu.verify_attn(0, 0, bits_dev(qb), lse=lse)
+    check(p, out, lse, qb, cap=cap)
+    p.close()
+
+
+@pytest.mark.parametrize("scale,cap", [(30.0, 2000.0), (300.0, 2000.0), (-2.0, 100.0), (0.0, 1e6)])
+def test_scores_around_a_large_cap(cuda_device, scale, cap):
+    """Scores on both sides of the kernel's two forms, up to far beyond the cap."""
+    for bits in (8, 16):
+        p = Pair(1, 4, 2, 64, 1, 8, 200, 3, bits=bits, seed=24, q_std=8.0, scale=scale).load().append(3)
+        p.gpu.set_scores(cap)
+        qb, lse = p.queries(3), p.lse(3)
+        out = p.gpu.verify_attn(0, 0, bits_dev(qb), lse=lse, scale=scale)
+        check(p, out, lse, qb, cap=cap)
+        p.close()
+
+
+def test_caps_that_fp32_cannot_hold_are_refused(cuda_device):
+    p = Pair(1, 2, 2, 64, 1, 8, 100, 3, bits=16).load().append(3)
+    for cap in (1.1e36, 1e38, 3e38):
+        with pytest.raises(ripe.RipeError) as e:
+            p.gpu.set_scores(cap)
+        assert e.value.status == ripe.RIPE_EINVAL
+    p.gpu.set_scores(1e-39)  # a subnormal cap: 0 in the kernel's arithmetic
+    with pytest.raises(ripe.RipeError) as e:
+        p.gpu.verify_attn(0, 0, bits_dev(p.queries(3)), scale=1e-3)
+    assert e.value.status == ripe.RIPE_EINVAL
     p.close()
