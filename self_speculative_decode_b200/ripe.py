@@ -144,11 +144,13 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _dev(t, dtype, shape, name):
-    """Address of a contiguous CUDA tensor of this dtype and (unless None) shape."""
+def _dev(t, dtype, shape, name, device=None):
+    """Address of a contiguous CUDA tensor of this dtype and (unless None) shape, on the device with this number."""
     torch = _torch or _load_torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the cache on cuda:{device}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -437,15 +439,15 @@ class RipeCache:
         torch = _torch or _load_torch()
         ld_t = k.shape[2]
         shape = (self.N, self.kvH, ld_t, self.d)
-        ripe_load_prefix(self.handle, layer, plane, list(T), _dev(k, torch.bfloat16, shape, "k"),
-                         _dev(v, torch.bfloat16, shape, "v"), ld_t, self._on(stream))
+        ripe_load_prefix(self.handle, layer, plane, list(T), _dev(k, torch.bfloat16, shape, "k", self.device),
+                         _dev(v, torch.bfloat16, shape, "v", self.device), ld_t, self._on(stream))
 
     def append_block(self, layer, r, k, v, stream=None):
         torch = _torch or _load_torch()
         B = k.shape[1]
         shape = (self.N, B, self.kvH, self.d)
-        ripe_append_block(self.handle, layer, r, B, _dev(k, torch.bfloat16, shape, "k"),
-                          _dev(v, torch.bfloat16, shape, "v"), self._on(stream))
+        ripe_append_block(self.handle, layer, r, B, _dev(k, torch.bfloat16, shape, "k", self.device),
+                          _dev(v, torch.bfloat16, shape, "v", self.device), self._on(stream))
 
     def set_scores(self, softcap=0.0, slopes=None, stream=None):
         """Capped scores (softcap > 0) and a bias -slopes[h] * distance (Hq floats) in every later attention call."""
@@ -493,11 +495,11 @@ class RipeCache:
         torch = _torch or _load_torch()
         B = q.shape[1]
         shape = (self.N, B, self.Hq, self.d)
-        qp = _dev(q, torch.bfloat16, shape, "q")
+        qp = _dev(q, torch.bfloat16, shape, "q", self.device)
         if out is None:
             out = torch.empty_like(q)  # contiguous, as q
-        op = _dev(out, torch.bfloat16, shape, "out")
-        lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
+        op = _dev(out, torch.bfloat16, shape, "out", self.device)
+        lp = _dev(lse, torch.float32, shape[:3], "lse", self.device) if lse is not None else None
         ripe_verify_attn(self.handle, layer, r, qp, op, lp, scale, self._on(stream))
         return out
 
@@ -507,13 +509,13 @@ class RipeCache:
         B = q.shape[1]
         kshape = (self.N, B, self.kvH, self.d)
         shape = (self.N, B, self.Hq, self.d)
-        kp = _dev(k, torch.bfloat16, kshape, "k")
-        vp = _dev(v, torch.bfloat16, kshape, "v")
-        qp = _dev(q, torch.bfloat16, shape, "q")
+        kp = _dev(k, torch.bfloat16, kshape, "k", self.device)
+        vp = _dev(v, torch.bfloat16, kshape, "v", self.device)
+        qp = _dev(q, torch.bfloat16, shape, "q", self.device)
         if out is None:
             out = torch.empty_like(q)  # contiguous, as q
-        op = _dev(out, torch.bfloat16, shape, "out")
-        lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
+        op = _dev(out, torch.bfloat16, shape, "out", self.device)
+        lp = _dev(lse, torch.float32, shape[:3], "lse", self.device) if lse is not None else None
         ripe_append_verify(self.handle, layer, r, B, kp, vp, qp, op, lp, scale, self._on(stream))
         return out
 
@@ -525,13 +527,13 @@ class RipeCache:
         torch = _torch or _load_torch()
         kshape = (self.N, 1, self.kvH, self.d)
         shape = (self.N, 1, self.Hq, self.d)
-        kp = _dev(k, torch.bfloat16, kshape, "k")
-        vp = _dev(v, torch.bfloat16, kshape, "v")
-        qp = _dev(q, torch.bfloat16, shape, "q")
+        kp = _dev(k, torch.bfloat16, kshape, "k", self.device)
+        vp = _dev(v, torch.bfloat16, kshape, "v", self.device)
+        qp = _dev(q, torch.bfloat16, shape, "q", self.device)
         if out is None:
             out = torch.empty_like(q)  # contiguous, as q
-        op = _dev(out, torch.bfloat16, shape, "out")
-        lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
+        op = _dev(out, torch.bfloat16, shape, "out", self.device)
+        lp = _dev(lse, torch.float32, shape[:3], "lse", self.device) if lse is not None else None
         if sink is None and window is None:
             ripe_draft_attn(self.handle, layer, r, j, kp, vp, qp, op, lp, scale, self._on(stream))
         else:
@@ -544,11 +546,11 @@ class RipeCache:
         torch = _torch or _load_torch()
         B = q.shape[1]
         shape = (self.N, B, self.Hq, self.d)
-        qp = _dev(q, torch.bfloat16, shape, "q")
+        qp = _dev(q, torch.bfloat16, shape, "q", self.device)
         if out is None:
             out = torch.empty_like(q)  # contiguous, as q
-        op = _dev(out, torch.bfloat16, shape, "out")
-        lp = _dev(lse, torch.float32, shape[:3], "lse") if lse is not None else None
+        op = _dev(out, torch.bfloat16, shape, "out", self.device)
+        lp = _dev(lse, torch.float32, shape[:3], "lse", self.device) if lse is not None else None
         ripe_verify_attn_wave(self.handle, layer, list(loop_of_position), qp, op, lp, scale, self._on(stream))
         return out
 
@@ -557,7 +559,7 @@ class RipeCache:
 
     def commit_device(self, accepted, stream=None):
         torch = _torch or _load_torch()
-        ripe_commit_device(self.handle, _dev(accepted, torch.int32, (self.N,), "accepted"), self._on(stream))
+        ripe_commit_device(self.handle, _dev(accepted, torch.int32, (self.N,), "accepted", self.device), self._on(stream))
 
     def sync_lengths(self, stream=None):
         return ripe_sync_lengths(self.handle, self.N, self._on(stream))
@@ -572,7 +574,7 @@ class RipeCache:
         if not st["lengths_synced"]:
             raise RipeError(RIPE_ESTATE, "export")
         Tv = self.sync_lengths(stream)[n] + st["block_len"]
-        dev = torch.device("cuda", torch.cuda.current_device())
+        dev = torch.device("cuda", self.device)
         k = torch.zeros((self.R, self.kvH, Tv, self.d), dtype=torch.bfloat16, device=dev)
         v = torch.zeros_like(k)
         present = torch.zeros((self.R, Tv), dtype=torch.uint8, device=dev)
@@ -586,7 +588,7 @@ class RipeCache:
         if not self.stats()["lengths_synced"]:
             raise RipeError(RIPE_ESTATE, "export_q8")
         blocks = max(0, self.sync_lengths(stream)[n] - self.W) // 64
-        dev = torch.device("cuda", torch.cuda.current_device())
+        dev = torch.device("cuda", self.device)
         k, v = (torch.empty((self.kvH, 64 * blocks, self.d), dtype=torch.int8, device=dev) for _ in range(2))
         ks, vs = (torch.empty((self.kvH, blocks), dtype=torch.float32, device=dev) for _ in range(2))
         if blocks or self.kv_bits != 8:
