@@ -144,6 +144,18 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _made(make, stream, device):
+    """make() with the call's stream current: a tensor belongs to the stream that is current when it is allocated, and
+    memory that another one still uses, or clears, is no place for this call's results."""
+    if stream is None:
+        return make()
+    torch = _torch or _load_torch()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def _dev(t, dtype, shape, name, device=None):
     """Address of a contiguous CUDA tensor of this dtype and (unless None) shape, on the device with this number."""
     torch = _torch or _load_torch()
@@ -384,7 +396,7 @@ def append_rope_static(view, layer, r, k, v, q=None, table=None, q_out=None, dev
         shape = (N, B, view.q_heads, view.head_dim)
         qp, ld_q = _rows(q, torch.bfloat16, shape, "q")
         if q_out is None:
-            q_out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            q_out = _made(lambda: torch.empty(shape, dtype=torch.bfloat16, device=q.device), stream, here)
         qo = _dev(q_out, torch.bfloat16, shape, "q_out")
     ripe_append_rope_static(view, layer, r, kp, vp, ld_kv, qp, ld_q, qo, None if table is None else table.rope,
                             _dev(device_error, torch.int32, (1,), "device_error"), stream)
@@ -393,6 +405,9 @@ def append_rope_static(view, layer, r, k, v, q=None, table=None, q_out=None, dev
 
 class RipeCache:
     """A RIPE cache on the current CUDA device, driven with torch tensors.
+
+    A call runs on ``stream`` (a torch stream, or its handle as an int), or on the current stream of the cache's device;
+    what it allocates for its results belongs to that stream.
 
     ``kv_bits``: 16, or 8 to hold the deepest-plane region in 8 bits with a scale for each 64 positions.
 
@@ -466,7 +481,7 @@ class RipeCache:
         vp, ld_v = _rows(v, torch.bfloat16, (self.N, B, self.kvH, self.d), "v")
         if ld_v != ld_kv:
             raise ValueError("k and v must have the same token stride")
-        qp, ld_q, q_out, qo = self._rotated(q, q_out, B, self.Hq, "q")
+        qp, ld_q, q_out, qo = self._rotated(q, q_out, B, self.Hq, "q", stream)
         self._here(k, v, q, q_out, table.cos, table.sin)
         ripe_append_block_rope(self.handle, layer, r, B, kp, vp, ld_kv, qp, ld_q, qo, table.rope, self._on(stream))
         return q_out
@@ -475,20 +490,20 @@ class RipeCache:
         """k [N][B][kvH][d] and q [N][B][Hq][d] of block positions j .. j + B - 1 rotated, for the draft calls and
         append_verify; returns (k_out, q_out)."""
         B = (k if k is not None else q).shape[1]
-        kp, ld_k, k_out, ko = self._rotated(k, k_out, B, self.kvH, "k")
-        qp, ld_q, q_out, qo = self._rotated(q, q_out, B, self.Hq, "q")
+        kp, ld_k, k_out, ko = self._rotated(k, k_out, B, self.kvH, "k", stream)
+        qp, ld_q, q_out, qo = self._rotated(q, q_out, B, self.Hq, "q", stream)
         self._here(k, q, k_out, q_out, table.cos, table.sin)
         ripe_rotate_block(self.handle, j, B, kp, ld_k, ko, qp, ld_q, qo, table.rope, self._on(stream))
         return k_out, q_out
 
-    def _rotated(self, x, x_out, B, heads, name):
+    def _rotated(self, x, x_out, B, heads, name, stream):
         torch = _torch or _load_torch()
         if x is None:
             return None, 0, None, None
         shape = (self.N, B, heads, self.d)
         p, ld = _rows(x, torch.bfloat16, shape, name)
         if x_out is None:
-            x_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            x_out = _made(lambda: torch.empty(shape, dtype=torch.bfloat16, device=x.device), stream, self.device)
         return p, ld, x_out, _dev(x_out, torch.bfloat16, shape, name + "_out")
 
     def verify_attn(self, layer, r, q, out=None, lse=None, scale=1.0, stream=None):
@@ -497,7 +512,7 @@ class RipeCache:
         shape = (self.N, B, self.Hq, self.d)
         qp = _dev(q, torch.bfloat16, shape, "q", self.device)
         if out is None:
-            out = torch.empty_like(q)  # contiguous, as q
+            out = _made(lambda: torch.empty_like(q), stream, self.device)  # contiguous, as q
         op = _dev(out, torch.bfloat16, shape, "out", self.device)
         lp = _dev(lse, torch.float32, shape[:3], "lse", self.device) if lse is not None else None
         ripe_verify_attn(self.handle, layer, r, qp, op, lp, scale, self._on(stream))
@@ -513,7 +528,7 @@ class RipeCache:
         vp = _dev(v, torch.bfloat16, kshape, "v", self.device)
         qp = _dev(q, torch.bfloat16, shape, "q", self.device)
         if out is None:
-            out = torch.empty_like(q)  # contiguous, as q
+            out = _made(lambda: torch.empty_like(q), stream, self.device)  # contiguous, as q
         op = _dev(out, torch.bfloat16, shape, "out", self.device)
         lp = _dev(lse, torch.float32, shape[:3], "lse", self.device) if lse is not None else None
         ripe_append_verify(self.handle, layer, r, B, kp, vp, qp, op, lp, scale, self._on(stream))
@@ -531,7 +546,7 @@ class RipeCache:
         vp = _dev(v, torch.bfloat16, kshape, "v", self.device)
         qp = _dev(q, torch.bfloat16, shape, "q", self.device)
         if out is None:
-            out = torch.empty_like(q)  # contiguous, as q
+            out = _made(lambda: torch.empty_like(q), stream, self.device)  # contiguous, as q
         op = _dev(out, torch.bfloat16, shape, "out", self.device)
         lp = _dev(lse, torch.float32, shape[:3], "lse", self.device) if lse is not None else None
         if sink is None and window is None:
@@ -548,7 +563,7 @@ class RipeCache:
         shape = (self.N, B, self.Hq, self.d)
         qp = _dev(q, torch.bfloat16, shape, "q", self.device)
         if out is None:
-            out = torch.empty_like(q)  # contiguous, as q
+            out = _made(lambda: torch.empty_like(q), stream, self.device)  # contiguous, as q
         op = _dev(out, torch.bfloat16, shape, "out", self.device)
         lp = _dev(lse, torch.float32, shape[:3], "lse", self.device) if lse is not None else None
         ripe_verify_attn_wave(self.handle, layer, list(loop_of_position), qp, op, lp, scale, self._on(stream))
@@ -575,9 +590,9 @@ class RipeCache:
             raise RipeError(RIPE_ESTATE, "export")
         Tv = self.sync_lengths(stream)[n] + st["block_len"]
         dev = torch.device("cuda", self.device)
-        k = torch.zeros((self.R, self.kvH, Tv, self.d), dtype=torch.bfloat16, device=dev)
-        v = torch.zeros_like(k)
-        present = torch.zeros((self.R, Tv), dtype=torch.uint8, device=dev)
+        k, v, present = _made(lambda: (*(torch.zeros((self.R, self.kvH, Tv, self.d), dtype=torch.bfloat16, device=dev)
+                                         for _ in range(2)),
+                                       torch.zeros((self.R, Tv), dtype=torch.uint8, device=dev)), stream, self.device)
         if Tv:
             ripe_cache_export(self.handle, n, layer, k.data_ptr(), v.data_ptr(), present.data_ptr(), self._on(stream))
         return k, v, present
@@ -589,8 +604,10 @@ class RipeCache:
             raise RipeError(RIPE_ESTATE, "export_q8")
         blocks = max(0, self.sync_lengths(stream)[n] - self.W) // 64
         dev = torch.device("cuda", self.device)
-        k, v = (torch.empty((self.kvH, 64 * blocks, self.d), dtype=torch.int8, device=dev) for _ in range(2))
-        ks, vs = (torch.empty((self.kvH, blocks), dtype=torch.float32, device=dev) for _ in range(2))
+        k, v, ks, vs = _made(lambda: [torch.empty((self.kvH, 64 * blocks, self.d), dtype=torch.int8, device=dev)
+                                      for _ in range(2)] +
+                                     [torch.empty((self.kvH, blocks), dtype=torch.float32, device=dev) for _ in range(2)],
+                             stream, self.device)
         if blocks or self.kv_bits != 8:
             ripe_cache_export_q8(self.handle, n, layer, k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), self._on(stream))
         return k, v, ks, vs

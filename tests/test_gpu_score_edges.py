@@ -254,3 +254,34 @@ def test_caps_that_fp32_cannot_hold_are_refused(cuda_device):
         p.gpu.verify_attn(0, 0, bits_dev(p.queries(3)), scale=1e-3)
     assert e.value.status == ripe.RIPE_EINVAL
     p.close()
+
+
+# ------------------------------------------------------------------ results on a side stream
+@pytest.mark.parametrize("as_int", [False, True])
+def test_results_of_a_side_stream_are_allocated_on_it(cuda_device, as_int):
+    """While the default stream still uses memory that it has given back, and clears new memory only later."""
+    p = Pair(2, 4, 2, 64, 2, 8, [200, 131], 3, bits=8, seed=5).load().append(3)
+    angle = torch.arange(300, device="cuda")[:, None] * 0.01 ** (torch.arange(32, device="cuda") / 32)
+    t = ripe.RotaryTable(angle.cos(), angle.sin())
+    q, k = bits_dev(p.queries(3)), torch.randn((2, 3, 2, 64), device="cuda").bfloat16()
+    s = torch.cuda.Stream()
+
+    def calls(stream):
+        return [p.gpu.verify_attn(0, 0, q, stream=stream), p.gpu.verify_attn_wave(0, [0, 1, 0], q, stream=stream),
+                *p.gpu.rotate_block(0, t, k, q, stream=stream), *p.gpu.export(0, 0, stream=stream),
+                *p.gpu.export_q8(0, 0, stream=stream), *p.gpu.export(1, 0, stream=stream)]
+
+    want = [x.clone() for x in calls(None)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(100_000_000)
+        used = [torch.empty_like(x) for x in want]
+        for x in used:
+            x.fill_(7)
+        del used, x
+        got = calls(s.cuda_stream if as_int else s)
+        s.synchronize()
+        torch.cuda.synchronize()  # the default stream fills its memory only now
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del got
+    p.close()
