@@ -25,7 +25,9 @@
 //     that stream the keys one after the other, each a head of its own in the tile lists.
 //   * The K scale enters with the softmax scale; the V scale enters the exponent: p' = 2^(x + log2 s -
 //     m), O sums p' u, and the normaliser sums p' / s.  So a block costs no multiply of its own per
-//     element, and the reference m follows the size of p' u, which is what O accumulates.
+//     element, and the reference m follows the size of p' u, which is what O accumulates.  s spans 2^-80 to 2^80:
+//     where p' leaves fp32 the key's weight still counts.  Blocks with s below kTinyScale take their share of the
+//     normaliser from 2^(x - m), and where it is rescaled by less than fp32 holds that goes in two steps.
 //   * tanh y = 1 - 2 / (1 + e^2y): one exponential and one reciprocal, absolute error 2^-22 of the cap
 //     (the hardware's tanh is 2^-11 relative: 0.02 at a cap of 50).  That error moves the weights as much however
 //     small the scores are, so that caps from kCapSeries on take the odd series where |y| is small (capped): an
@@ -51,6 +53,9 @@ namespace ripe {
 // softmax reference: moved when a score exceeds it by more than kHi, and then to kLo below the maximum, so
 // that the probabilities lie in (0, 2^15], within f16's range, and are exact down to 2^-(14 + 10 + kLo)
 constexpr float kScoreHi = 15.f, kScoreLo = 7.f;
+// log2 of the smallest V scale whose p' / s is summed: beside values of the largest scale the reference is at most
+// 2^73 times the largest weight, and p' of that weight at least 2^-93, 33 bits above what fp32 flushes to zero
+constexpr float kTinyScale = -20.f;
 
 // Query-side shapes as VCfg (ripe_verify.cu): NQT 8-query tiles per warp, WR row groups, WK key groups
 // per 64-key block, TG tile groups consuming alternate tiles.
@@ -715,10 +720,10 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
 #pragma unroll
             for (int w = 0; w < C::NP; ++w) {
                 const float4 ml = *reinterpret_cast<const float4 *>(&mml[((w * WR + rgi) * C::NQ + q) * 4]);
-                const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-                if (!C::WIDE || w % WK == 0) wq[i * C::NPF + (C::WIDE ? w / WK : w)] = f;
-                L += f * ml.y;
-                Ll += f * ml.z;
+                const float h = ml.x == -INFINITY ? 0.f : exp2f(0.5f * (ml.x - M));  // twice: the sums may be large
+                if (!C::WIDE || w % WK == 0) wq[i * C::NPF + (C::WIDE ? w / WK : w)] = h * h;
+                L += h * ml.y * h;
+                Ll += h * ml.z * h;
             }
             *reinterpret_cast<float4 *>(&fin[i * 4]) = make_float4(M, L, Ll, 0.f);
         }
@@ -778,10 +783,10 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                     if (c >= nparts) continue;
                     // a partial of weight 0 is added all the same: one that has seen a NaN alone has no maximum, and
                     // its NaN has to reach the row
-                    const float w = ml[c].x == -INFINITY ? 0.f : exp2f(ml[c].x - M);
+                    const float h = ml[c].x == -INFINITY ? 0.f : exp2f(0.5f * (ml[c].x - M)), w = h * h;
                     acc.x += w * v[c].x; acc.y += w * v[c].y; acc.z += w * v[c].z; acc.w += w * v[c].w;
-                    L += w * ml[c].y;
-                    Ll += w * ml[c].z;
+                    L += h * ml[c].y * h;
+                    Ll += h * ml[c].z * h;
                 }
                 write_row(p, i, 4 * cx, acc, M, L, Ll);
             }
@@ -805,10 +810,10 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             for (int c = 0; c < nparts; ++c) {
                 const float mk = pw[c * C::ROWS + i];
                 const size_t prow = (static_cast<size_t>(c_first + c) + p) * C::ROWS + i;
-                const float w = mk == -INFINITY ? 0.f : exp2f(mk - M);
-                pw[c * C::ROWS + i] = w;
-                L += w * pl[c * C::ROWS + i];
-                Ll += w * __ldcg(&a.part_ml[prow * 4 + 2]);
+                const float h = mk == -INFINITY ? 0.f : exp2f(0.5f * (mk - M));
+                pw[c * C::ROWS + i] = h * h;
+                L += h * pl[c * C::ROWS + i] * h;
+                Ll += h * __ldcg(&a.part_ml[prow * 4 + 2]) * h;
             }
             fin[i * 4] = M;
             fin[i * 4 + 1] = L;
@@ -1099,9 +1104,11 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         }
     };
 
-    // moves a column's reference up by `up` (al: what its sums are worth then)
-    auto move_ref = [&](int nq, int e, float up, float al, float (&x)[C::SB][NQT][4]) {
+    // moves a column's reference up by `up`; its sums are worth 2^lg of what they were then
+    auto move_ref = [&](int nq, int e, float up, float lg, float (&x)[C::SB][NQT][4]) {
+        const float al = exp2f(fmaxf(lg, -100.f));  // (O is as good as 0 then)
         l_lse[nq][e] *= al;
+        if (lg < -100.f) l_lse[nq][e] *= exp2f(lg + 100.f);
         if constexpr (C::WIDE) {
             const int col = 8 * nq + 2 * c4 + e;
             if (g4 == 0) gfix[warp * C::NQ + col] *= al;
@@ -1120,6 +1127,16 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             o[mt][nq][e] *= al;
             o[mt][nq][e + 2] *= al;
         }
+    };
+    // a block with a tiny V scale: its keys' weights to the normaliser, in place of the sums that add_sums adds
+    auto sum_tiny = [&](const float (&x)[C::SB][NQT][4], const Scales &sc) {
+#pragma unroll
+        for (int nq = 0; nq < NQT; ++nq)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int sb = 0; sb < C::SB; ++sb)
+                    l_lse[nq][e] += exp2f(x[sb][nq][e] - sc.lv) + exp2f(x[sb][nq][e + 2] - sc.lv);
     };
     auto column_max = [&](const float (&x)[C::SB][NQT][4], int nq, int e) {
         float m = -INFINITY;
@@ -1146,8 +1163,9 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
         }
         relative(dsc, t0, cnt, kg * C::SB, sc, x, fast_tag, half_tag);
         // The reference moves when a score exceeds it by more than kScoreHi, or when the column has no sum
-        // yet; the warp looks at a column's maximum over all lanes only if one lane calls for it.
-        bool over = false;
+        // yet; the warp looks at a column's maximum over all lanes only if one lane calls for it (blocks of tiny
+        // values, as rare, are dealt with there too).
+        bool over = HALF && sc.lv < kTinyScale;
 #pragma unroll
         for (int nq = 0; nq < NQT; ++nq)
 #pragma unroll
@@ -1165,8 +1183,9 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                         l = fmaxf(l, __shfl_xor_sync(0xffffffffu, l, s));
                     }
                     if (mt > (l == 0.f ? -INFINITY : kScoreHi))
-                        move_ref(nq, e, mt - kScoreLo, l == 0.f ? 1.f : exp2f(kScoreLo - mt), x);
+                        move_ref(nq, e, mt - kScoreLo, l == 0.f ? 0.f : kScoreLo - mt, x);
                 }
+            if (HALF && sc.lv < kTinyScale) sum_tiny(x, sc);
         }
         float tl[NQT][2], tr[NQT][2];
 #pragma unroll
@@ -1185,7 +1204,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             }
             accumulate(dsc, kb0, t0, cnt, kb, 0, pb, fast_tag, half_tag);
         }
-        add_sums(tl, tr, sc.iv, fast_tag, half_tag);
+        add_sums(tl, tr, HALF && sc.lv < kTinyScale ? 0.f : sc.iv, fast_tag, half_tag);
     };
 
     // ---------------------------------------------------------------- a block, by the four warps of a wide group
@@ -1245,7 +1264,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             aborted = true;
             return;
         }
-        if (static_cast<int>(nblk & 1 ? flags.y : flags.x) == nblk) {
+        if (static_cast<int>(nblk & 1 ? flags.y : flags.x) == nblk || (HALF && scales_of(kb0).lv < kTinyScale)) {
             float *gm = gmax + tg * 4 * C::NQ;
 #pragma unroll
             for (int nq = 0; nq < NQT; ++nq)
@@ -1265,11 +1284,16 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
                     const float mt = fmaxf(fmaxf(g[0], g[C::NQ]), fmaxf(g[2 * C::NQ], g[3 * C::NQ]));
                     const bool has = seen >> (2 * nq + e) & 1;
                     if (mt > (has ? kScoreHi : -INFINITY)) {
-                        move_ref(nq, e, mt - kScoreLo, has ? exp2f(kScoreLo - mt) : 1.f, x);
+                        move_ref(nq, e, mt - kScoreLo, has ? kScoreLo - mt : 0.f, x);
                         seen |= 1u << (2 * nq + e);
                     }
                 }
             if (mine) put();
+            if (HALF && scales_of(kb0).lv < kTinyScale) {
+                sum_tiny(x, scales_of(kb0));
+#pragma unroll
+                for (int nq = 0; nq < NQT; ++nq) tl[nq][0] = tl[nq][1] = 0.f;
+            }
             named_bar_sync(2 + tg, 128);
         }
         if (16 * C::MT * kg < D) {

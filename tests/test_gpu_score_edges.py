@@ -14,8 +14,9 @@ def dense(p, q, n, j, cap=0.0, slopes=None):
     with one plane (R = 1), the deepest one for every key.
 
     Tolerances as score_ref's: eps is the error of a score, and what the cap adds to it 2^-21 of a cap below 64, 2^-19 of
-    the score from 64 on (csrc/ripe_score_kernel.cuh).  The largest probability is at least 2^7 (the reference moves to
-    2^-7 of the maximum), the smallest f16 step 2^-24: a weight is also off by up to 2^-25 / 2^7 = 2^-32 absolute."""
+    the score from 64 on (csrc/ripe_score_kernel.cuh).  The largest p' (a weight times its block's V
+    scale) is at least 2^7, the reference being 2^-7 of the maximum, and f16 holds each of them to 2^-25 absolute: a
+    key's p' u is off by up to 2^-32 of the largest value."""
     end, D = p.T[n] + j + 1, p.D(n)
     kv = []
     for w in range(2):
@@ -39,7 +40,8 @@ def dense(p, q, n, j, cap=0.0, slopes=None):
     w /= w.sum(1, keepdims=True)
     out = np.einsum("ht,htd->hd", w, kv[1])
     A, B = np.einsum("ht,htd->hd", w, abs(kv[1] - out[:, None])), np.einsum("ht,htd->hd", w, abs(kv[1]))
-    tol = 2.0 ** -8 * (abs(out) + A) + (2.0 ** -11 + 2 * eps[:, None] + 2.0 ** -18) * B + 2.0 ** -32 * abs(kv[1]).sum(1)
+    tol = 2.0 ** -8 * (abs(out) + A) + (2.0 ** -11 + 2 * eps[:, None] + 2.0 ** -18) * B \
+        + 2.0 ** -32 * end * abs(kv[1]).max()
     return out, tol, lse, eps + 2.0 ** -18 + 2.0 ** -22 * abs(lse)
 
 
@@ -284,4 +286,22 @@ def test_results_of_a_side_stream_are_allocated_on_it(cuda_device, as_int):
         torch.cuda.synchronize()  # the default stream fills its memory only now
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         del got
+    p.close()
+
+
+# ------------------------------------------------------------------ blocks of very different sizes
+# V of six blocks; a key's weight does not depend on its value's size, and rows of zeros count as any other
+@pytest.mark.parametrize("sizes", [(1e20, 0.0, 1.0, 1e-3, 0.0, 1.0), (0.0, 1e24, 0.0, 0.0, 1.0, 1e24),
+                                   (1e24, 1e-25, 1e24, 0.0, 1e24, 1e-20), (1e-25, 1e24, 1.0, 0.0, 1e-24, 0.0)])
+@pytest.mark.parametrize("Hq,B,T", [(2, 1, 400), (4, 4, 400), (8, 4, 400), (8, 4, 2000)])
+def test_weights_of_blocks_of_zeros_beside_large_ones(cuda_device, sizes, Hq, B, T):
+    p = Pair(1, Hq, 1, 64, 1, 8, T, B, seed=6)
+    rng = np.random.default_rng(0)
+    for b in range((T - 8) // 64):
+        x = rng.standard_normal((1, 1, 64, 64)).astype(np.float32) * np.float32(sizes[b % 6])
+        p.planes[0][0][1][:, :, 64 * b: 64 * b + 64] = synth.f32_to_bf16_bits(x)
+    p.load().append(B)
+    qb, lse = p.queries(B), p.lse(B)
+    out = p.gpu.verify_attn(0, 0, bits_dev(qb), lse=lse)
+    check(p, out, lse, qb)
     p.close()
