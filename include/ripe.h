@@ -212,7 +212,8 @@ int ripe_rotate_block(ripe_cache_t *c, int j, int B, const void *k, int64_t ld_k
  *   softcap > 0    x <- softcap * tanh(x / softcap), softcap at most 1e36 (RIPE_EINVAL); off by at most
  *                  2^-21 softcap below 64, and from 64 on by 2^-19 |x|, beside the rounding of x
  *   slopes         host fp32[q_heads] or NULL: x <- x - slopes[h] * (p - t), a bias linear in the
- *                  distance (finite; copied before the call returns; synchronises the stream)
+ *                  distance (copied before the call returns; synchronises the stream); finite, also times
+ *                  log2(e) and, where negative, times max_T as well (RIPE_EINVAL)
  * softcap 0 and slopes NULL (the state after allocation) give plain scores again.  Not while the
  * stream is captured (RIPE_ESTATE); a captured graph keeps the softcap and the presence of slopes that it
  * was captured with, and reads the slopes of the last call.  With either, the draft calls and

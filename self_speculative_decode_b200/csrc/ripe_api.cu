@@ -256,9 +256,11 @@ extern "C" {
 int ripe_set_scores(ripe_cache_t *c, float softcap, const float *slopes, void *stream) {
     const NvtxRange nvtx_range("ripe_set_scores");
     if (!c || !(softcap >= 0.f) || softcap > kCapMost) return RIPE_EINVAL;
-    if (slopes)
-        for (int h = 0; h < c->Hq; ++h)
-            if (!std::isfinite(slopes[h])) return RIPE_EINVAL;
+    if (slopes)  // the kernels hold slopes in log2 units, and a negative one makes the oldest keys' scores the largest
+        for (int h = 0; h < c->Hq; ++h) {
+            const float s2 = slopes[h] * 1.4426950408889634f;
+            if (!std::isfinite(s2) || (s2 < 0.f && !std::isfinite(s2 * static_cast<float>(c->max_T)))) return RIPE_EINVAL;
+        }
     DeviceGuard g(c->device);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;

@@ -305,3 +305,27 @@ def test_weights_of_blocks_of_zeros_beside_large_ones(cuda_device, sizes, Hq, B,
     out = p.gpu.verify_attn(0, 0, bits_dev(qb), lse=lse)
     check(p, out, lse, qb)
     p.close()
+
+
+# ------------------------------------------------------------------ slopes
+def test_slopes_at_the_end_of_fp32(cuda_device):
+    """Slopes whose bias leaves fp32 where it matters are refused; the largest accepted ones still select their keys."""
+    for bits in (8, 16):
+        p = Pair(1, 2, 2, 64, 1, 8, 300, 3, bits=bits, seed=15).load().append(3)
+        for bad in ([3e38, 0.0], [0.0, -3e38], [-1e36, 0.0]):  # 303 * 1e36 * log2(e) is above 3.4e38
+            with pytest.raises(ripe.RipeError) as e:
+                p.gpu.set_scores(0.0, bad)
+            assert e.value.status == ripe.RIPE_EINVAL
+        slopes = [2e38, -5e35]
+        p.gpu.set_scores(0.0, slopes)
+        qb, lse = p.queries(3), p.lse(3)
+        out = p.gpu.verify_attn(0, 0, bits_dev(qb), lse=lse)
+        for j in range(3):  # head 0 reads its own key alone, head 1 the oldest one
+            for h, t in ((0, 300 + j), (1, 0)):
+                v = synth.bf16_bits_to_f32(p.planes[0][0][1][0, h, t])
+                if bits == 8 and t == 0:
+                    u, s = quantised(synth.bf16_bits_to_f32(p.planes[0][0][1][0, h:h + 1, :64]))
+                    v = u[0, 0].astype(np.float32) * s[0, 0]
+                got = out[0, j, h].float().cpu().numpy()
+                assert (abs(got - v) <= 2.0 ** -7 * abs(v)).all()
+        p.close()
