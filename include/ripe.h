@@ -21,7 +21,10 @@
  *     Host pointers are read before the call returns.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  All device
  *     work is enqueued on it; calls return after enqueueing.
- *   - bf16 tensors are IEEE bfloat16, contiguous, row-major in the order given.
+ *   - bf16 tensors are IEEE bfloat16, contiguous, row-major in the order given.  Keys and values (and exports of
+ *     them) are 16-byte aligned; q, out, lse and device int32 arrays 4-byte aligned, q 16-byte aligned for more than 8
+ *     query rows per kv head while RIPE_CONSUMER_TC is selected; what the rotating calls ask is said there.
+ *     RIPE_EINVAL otherwise.
  *   - Argument and state errors are detected on the host before anything is
  *     enqueued and leave the cache unchanged.  A failed launch returns
  *     RIPE_ECUDA.  Faults detected by a kernel (a wait that gave up, a block
@@ -131,7 +134,7 @@ int ripe_cache_alloc(int batch, int layers, int q_heads, int kv_heads, int head_
  * head); ring as for ripe_cache_alloc with S = min(W + max_B + 63, max_T) slots.  stats.deep_rows is the
  * capacity of the 8-bit region in positions.
  * On such a cache ripe_append_verify and the draft calls take two launches, and every attention call needs
- * 16-byte aligned tensors and a finite scale (RIPE_EINVAL).
+ * a finite scale (RIPE_EINVAL).
  */
 int ripe_cache_alloc_q8(int batch, int layers, int q_heads, int kv_heads, int head_dim, int loops, int window,
                         int max_T, int max_B, int window_mode, ripe_cache_t **out);
@@ -217,8 +220,8 @@ int ripe_rotate_block(ripe_cache_t *c, int j, int B, const void *k, int64_t ld_k
  * softcap 0 and slopes NULL (the state after allocation) give plain scores again.  Not while the
  * stream is captured (RIPE_ESTATE); a captured graph keeps the softcap and the presence of slopes that it
  * was captured with, and reads the slopes of the last call.  With either, the draft calls and
- * ripe_append_verify take two launches, the tensors of an attention call are 16-byte aligned, and scale * log2(e),
- * with a softcap below 64 also 2 scale * log2(e) / softcap, is finite in fp32 and softcap not subnormal (RIPE_EINVAL).
+ * ripe_append_verify take two launches, and every attention call needs a scale whose product with log2(e), with a
+ * softcap below 64 2 scale * log2(e) / softcap, is finite in fp32, and a softcap that is not subnormal (RIPE_EINVAL).
  */
 int ripe_set_scores(ripe_cache_t *c, float softcap, const float *slopes, void *stream);
 

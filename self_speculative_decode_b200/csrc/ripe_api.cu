@@ -101,14 +101,11 @@ size_t counter_bytes(const ripe_cache *c) { return 2 * static_cast<size_t>(c->N)
 
 int64_t block_rows(const ripe_cache *c, int B) { return static_cast<int64_t>(c->N) * B; }
 
-// the kernels of launch_score read queries in 8-byte and write outputs in 4-byte words
-bool aligned_io(const void *q, const void *out) {
-    return ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-}
-
-// What a call that launch_score serves asks of its arguments; checked before anything of the call is enqueued.
-int check_scored(const ripe_cache *c, const void *q, const void *out, float scale) {
-    return aligned_io(q, out) && std::isfinite(score_factor(c, scale)) ? RIPE_OK : RIPE_EINVAL;
+// What an attention call asks of its queries, outputs and scale, beside shapes: checked before anything is enqueued.
+// rows: query rows per kv head of a launch that the tcgen05 consumer may serve, else 0
+bool good_attn(const ripe_cache *c, const void *q, const void *out, const void *lse, float scale, int rows) {
+    if (c->plain()) return aligned_verify(q, out, lse, rows);
+    return aligned_to(4, q, out, lse) && std::isfinite(score_factor(c, scale));
 }
 
 // T_n + j + B positions of every sequence have to fit the cache and the rotation's table
@@ -308,7 +305,8 @@ int ripe_cache_free(ripe_cache_t *c) {
 int ripe_load_prefix(ripe_cache_t *c, int layer, int plane, const int32_t *T, const void *k, const void *v,
                      int64_t ld_t, void *stream) {
     const NvtxRange nvtx_range("ripe_load_prefix");
-    if (!c || !T || !k || !v || layer < 0 || layer >= c->L || plane < 0 || plane >= c->R) return RIPE_EINVAL;
+    if (!c || !T || !k || !v || layer < 0 || layer >= c->L || plane < 0 || plane >= c->R || !aligned_to(16, k, v))
+        return RIPE_EINVAL;
     if (c->B_cur != 0 || !c->synced || any_drafted(c)) return RIPE_ESTATE;
     int Tmax = 0;
     for (int n = 0; n < c->N; ++n) {
@@ -331,7 +329,8 @@ int ripe_load_prefix(ripe_cache_t *c, int layer, int plane, const int32_t *T, co
 
 int ripe_append_block(ripe_cache_t *c, int layer, int r, int B, const void *k, const void *v, void *stream) {
     const NvtxRange nvtx_range("ripe_append_block");
-    if (!c || !k || !v || layer < 0 || layer >= c->L || r < 0 || r >= c->R || B < 1 || B > c->max_B)
+    if (!c || !k || !v || layer < 0 || layer >= c->L || r < 0 || r >= c->R || B < 1 || B > c->max_B ||
+        !aligned_to(16, k, v))
         return RIPE_EINVAL;
     if (c->B_cur != 0 && B != c->B_cur) return RIPE_EINVAL;
     for (int n = 0; n < c->N; ++n)
@@ -384,7 +383,7 @@ int ripe_verify_attn(ripe_cache_t *c, int layer, int r, const void *q, void *out
     const NvtxRange nvtx_range("ripe_verify_attn");
     if (!c || !q || !out || layer < 0 || layer >= c->L || r < 0 || r >= c->R) return RIPE_EINVAL;
     if (c->B_cur == 0 || !c->appended[static_cast<size_t>(layer) * c->R + r]) return RIPE_ESTATE;
-    if (!c->plain() && check_scored(c, q, out, scale) != RIPE_OK) return RIPE_EINVAL;
+    if (!good_attn(c, q, out, lse, scale, c->B_cur * c->g)) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     if (!c->plain()) {
@@ -403,7 +402,7 @@ int ripe_append_verify(ripe_cache_t *c, int layer, int r, int B, const void *k, 
     if (c->B_cur != 0 && B != c->B_cur) return RIPE_EINVAL;
     for (int n = 0; n < c->N; ++n)
         if (c->T[n] + B > c->max_T) return RIPE_ECAPACITY;
-    if (!c->plain() && (check_scored(c, q, out, scale) != RIPE_OK || !aligned_io(k, v))) return RIPE_EINVAL;
+    if (!good_attn(c, q, out, lse, scale, 0) || !aligned_to(16, k, v)) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     if (!c->plain()) {
@@ -439,7 +438,7 @@ static int draft_step(ripe_cache_t *c, int layer, int r, int j, int sink, int wi
     if (c->B_cur != 0 || j > c->drafted[idx]) return RIPE_ESTATE;
     for (int n = 0; n < c->N; ++n)
         if (c->T[n] + j + 1 > c->max_T) return RIPE_ECAPACITY;
-    if (!c->plain() && (check_scored(c, q, out, scale) != RIPE_OK || !aligned_io(k, v))) return RIPE_EINVAL;
+    if (!good_attn(c, q, out, lse, scale, 0) || !aligned_to(16, k, v)) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     int st;
@@ -480,7 +479,7 @@ int ripe_verify_attn_wave(ripe_cache_t *c, int layer, const int32_t *loop_of_pos
         if (r < 0 || r >= c->R) return RIPE_EINVAL;
         if (!c->appended[static_cast<size_t>(layer) * c->R + r]) return RIPE_ESTATE;
     }
-    if (!c->plain() && check_scored(c, q, out, scale) != RIPE_OK) return RIPE_EINVAL;
+    if (!good_attn(c, q, out, lse, scale, c->B_cur * c->g)) return RIPE_EINVAL;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
     if (!c->plain()) {
@@ -509,7 +508,7 @@ int ripe_commit(ripe_cache_t *c, const int32_t *accepted_len, void *stream) {
 
 int ripe_commit_device(ripe_cache_t *c, const int32_t *accepted_len, void *stream) {
     const NvtxRange nvtx_range("ripe_commit_device");
-    if (!c || !accepted_len) return RIPE_EINVAL;
+    if (!c || !accepted_len || !aligned_to(4, accepted_len)) return RIPE_EINVAL;
     if (c->B_cur == 0 || !all_appended(c)) return RIPE_ESTATE;
     DeviceGuard g(c->device);
     if (!g.ok) return RIPE_ECUDA;
@@ -559,7 +558,8 @@ int ripe_cache_stats(const ripe_cache_t *c, ripe_stats *st) {
 int ripe_cache_export(ripe_cache_t *c, int n, int layer, void *k_out, void *v_out, uint8_t *plane_present,
                       void *stream) {
     const NvtxRange nvtx_range("ripe_cache_export");
-    if (!c || !k_out || !v_out || !plane_present || n < 0 || n >= c->N || layer < 0 || layer >= c->L)
+    if (!c || !k_out || !v_out || !plane_present || n < 0 || n >= c->N || layer < 0 || layer >= c->L ||
+        !aligned_to(16, k_out, v_out))
         return RIPE_EINVAL;
     if (!c->synced) return RIPE_ESTATE;
     DeviceGuard g(c->device);
@@ -571,7 +571,7 @@ int ripe_cache_export_q8(ripe_cache_t *c, int n, int layer, int8_t *k_out, int8_
                          float *v_scale, void *stream) {
     const NvtxRange nvtx_range("ripe_cache_export_q8");
     if (!c || c->kv_bits != 8 || !k_out || !v_out || !k_scale || !v_scale || n < 0 || n >= c->N || layer < 0 ||
-        layer >= c->L)
+        layer >= c->L || !aligned_to(4, k_scale, v_scale))
         return RIPE_EINVAL;
     if (!c->synced) return RIPE_ESTATE;
     DeviceGuard g(c->device);

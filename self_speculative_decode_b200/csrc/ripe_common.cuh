@@ -533,6 +533,15 @@ int ensure_verify_attributes(int device);
 // ripe_set_verify_consumer: the consumer of verification launches with 9..64 query rows per kv head
 int set_verify_consumer(int consumer);
 int get_verify_consumer();
+// Alignment of the tensors of a call, in bytes: what the kernels' loads and stores take.  Rows of keys and values move in
+// 16-byte words, q and out in 4-byte words; the tcgen05 consumer loads q in 16-byte words.
+inline bool aligned_to(uintptr_t bytes, const void *a, const void *b = nullptr, const void *c = nullptr) {
+    return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c)) &
+            (bytes - 1)) == 0;
+}
+inline bool aligned_verify(const void *q, const void *out, const void *lse, int rows) {
+    return aligned_to(4, q, out, lse) && (rows <= 8 || get_verify_consumer() != RIPE_CONSUMER_TC || aligned_to(16, q));
+}
 
 // Everything one verify launch needs, for callers that own the buffers and the scratch.
 struct RawVerify {

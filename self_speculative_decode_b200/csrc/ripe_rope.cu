@@ -292,7 +292,7 @@ extern "C" int ripe_append_rope_static(const ripe_cache_view *view, int layer, i
         c.q_heads % c.kv_heads || (d != 64 && d != 96 && d != 128) || c.loops < 1 || c.loops > kMaxLoops ||
         c.window < 0 || c.max_T < 1 || c.max_B < 1 || c.max_B > kMaxQueryRows || c.max_B > c.max_T ||
         c.max_B * (c.q_heads / c.kv_heads) > kMaxQueryRows || c.block_len < 1 || c.block_len > c.max_B ||
-        layer < 0 || layer >= c.layers || r < 0 || r >= c.loops || !c.k_ring || !c.v_ring || !c.lengths ||
+        layer < 0 || layer >= c.layers || r < 0 || r >= c.loops || !c.k_ring || !c.v_ring || !c.lengths || !aligned_to(4, c.lengths, device_error) ||
         !aligned16(c.k_ring) || !aligned16(c.v_ring))
         return RIPE_EINVAL;
     const int64_t rows = static_cast<int64_t>(c.batch) * c.block_len;

@@ -135,7 +135,8 @@ extern "C" int ripe_verify_attn_static(const ripe_cache_view *v, int layer, int 
         v->max_B > v->max_T || v->max_B * (Hq / kvH) > kMaxQueryRows || v->block_len < 1 ||
         v->block_len > v->max_B ||
         (v->window_mode != RIPE_WINDOW_QUERY_RELATIVE && v->window_mode != RIPE_WINDOW_CACHE_RELATIVE) ||
-        layer < 0 || layer >= L || r < 0 || r >= R || !v->k_ring || !v->v_ring || !v->lengths)
+        layer < 0 || layer >= L || r < 0 || r >= R || !v->k_ring || !v->v_ring || !v->lengths ||
+        !aligned_verify(q, out, lse, v->block_len * (Hq / kvH)) || !aligned_to(4, v->lengths, device_error))
         return RIPE_EINVAL;
     const int W = v->window > v->max_T ? v->max_T : v->window;
     const long long s_slots = static_cast<long long>(W) + v->max_B;
