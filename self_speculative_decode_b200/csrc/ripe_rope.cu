@@ -213,6 +213,11 @@ int check_rope(const ripe_rope *rope, int d, int Hq, int kvH, int64_t rows, cons
     if (q && k && overlaps(k, span_k, q_out, full_q)) return RIPE_EINVAL;
     if (q && v && overlaps(v, span_k, q_out, full_q)) return RIPE_EINVAL;
     if (q && k_out && (overlaps(q, span_q, k_out, full_k) || overlaps(q_out, full_q, k_out, full_k))) return RIPE_EINVAL;
+    if (rope) {  // the tables are inputs too: fp32, so twice as many elements of two bytes
+        const int64_t table = static_cast<int64_t>(rope->positions) * rope->rotary_dim;
+        for (const float *t : {rope->cos, rope->sin})
+            if ((q && overlaps(t, table, q_out, full_q)) || (k_out && overlaps(t, table, k_out, full_k))) return RIPE_EINVAL;
+    }
     return RIPE_OK;
 }
 

@@ -94,3 +94,14 @@ def test_queries_of_the_tcgen05_consumer(cuda_device):
     finally:
         ripe.ripe_set_verify_consumer(before)
     c.close()
+
+
+@pytest.mark.parametrize("q_out", [1 << 22, (1 << 22) + 100 * 64 * 2 - 16, (1 << 22) - 2048 * 2 + 16, (1 << 23) + 64])
+def test_queries_rotated_onto_a_table(q_out):
+    """q_out [2][4][4][64] over any part of a table of 100 positions x 32 fp32."""
+    view = ripe.CacheView(batch=2, layers=1, q_heads=4, kv_heads=2, head_dim=64, loops=2, window=8, max_T=100, max_B=4,
+                          window_mode=0, block_len=4, k_ring=1 << 20, v_ring=2 << 20, lengths=4 << 20)
+    rope = ripe.Rope(cos=1 << 22, sin=1 << 23, positions=100, rotary_dim=64, interleaved=0)
+    vp = ctypes.c_void_p
+    assert ripe.lib().ripe_append_rope_static(ctypes.byref(view), 0, 0, vp(4096), vp(8192), 128, vp(1 << 24), 256, vp(q_out),
+                                              ctypes.byref(rope), vp(64), vp(0)) == ripe.RIPE_EINVAL
