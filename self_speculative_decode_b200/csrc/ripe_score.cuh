@@ -223,7 +223,6 @@ struct ScoreArgs {
     float cap;            // cap * log2(e), 0: no cap
     float rcap;           // 1 / cap for a cap from kCapSeries on, else 0
     int dbg_deep_rows, dbg_part_slots;
-    long long dbg_ring_pages;
 };
 
 cudaError_t launch_score_q8(int d, const LaunchTarget &t, int grid, const ScoreArgs &a, cudaStream_t s);
