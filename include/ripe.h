@@ -195,7 +195,9 @@ typedef struct ripe_rope {
  *   ld_kv, ld_q  multiples of 8, at least kv_heads * d and q_heads * d: parts of one projection's output
  *            can be passed in place
  * Pointers are 16-byte aligned; q_out is q itself (packed) or overlaps no input (else RIPE_EINVAL).
- * State rules and errors as for ripe_append_block; RIPE_ECAPACITY also if T_n + B > rope->positions.
+ * State rules and errors as for ripe_append_block; RIPE_ECAPACITY also if T_n + B > rope->positions.  A captured step
+ * that is replayed past the table's end sets RIPE_DEVERR_CAPACITY and writes no rows, but a commit, which knows
+ * nothing of the table, still accepts them: give it max_T positions.
  */
 int ripe_append_block_rope(ripe_cache_t *c, int layer, int r, int B, const void *k, const void *v, int64_t ld_kv,
                            const void *q, int64_t ld_q, void *q_out, const ripe_rope *rope, void *stream);

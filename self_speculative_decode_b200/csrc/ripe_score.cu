@@ -76,12 +76,8 @@ int launch_score(ripe_cache *c, const ScoreCall &call, cudaStream_t s) {
     p.deep_box = c->deep_box;
     p.deep_tile = q8 && !wide ? 2 * kQ8Block : kTileRows;
     p.ring_box = wide && c->ring_box > kWideRingRows ? kWideRingRows : c->ring_box;
-    // A masked tile takes about as long as two deepest-plane tiles, and the end of a head (merging the warps' partials,
-    // the next head's queries) as long as 4, or 8 where 9 to 32 rows leave less of a tile's time to the copies.
-    // Measured on uneven batches of 32 sequences (10 .. 9000 keys; 8-bit: 4, 16 and 32 rows a kv head): 60, 68 and
-    // 60 us, against 107, 151 and 150 us with every tile at 1 and heads at 0.
-    p.ring_cost = 2;
-    p.head_cost = q8 && a.grows > 8 ? 8 : 4;
+    p.ring_cost = score_ring_cost();
+    p.head_cost = score_head_cost(q8, a.grows);
     p.crel = c->mode == RIPE_WINDOW_CACHE_RELATIVE ? 1 : 0;
     p.sink = call.sink;
     p.dwin = call.window;

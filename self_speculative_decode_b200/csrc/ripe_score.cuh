@@ -72,6 +72,17 @@ struct ScoreGeom {
     int cost;  // of the whole list, in DEEP tiles
 };
 
+// A masked tile takes about as long as two deepest-plane tiles, and the end of a head (merging the warps' partials, the
+// next head's queries) as long as 4 or more, growing with the rows.  Measured on 32 sequences of 10 .. 9000 keys, 8 kv
+// heads x 128, at 4 / 16 / 32 / 64 rows a kv head, us:
+//   8 bits        59 /  81 / 155 / 295; heads at 4: 59 / 80 / 191 / 383, at 12: 59 /  83 / 134 / 247; masked tiles at 1:
+//                 59 /  79 / 173 / 330, at 3: 60 / 82 / 144 / 278
+//   bf16, capped  95 / 123 / 165 / 293; heads at 2: 106 / 143 / 191 / 336, at 8: 97 / 107 / 128 / 239; masked tiles at
+//                 1: 99 / 143 / 189 / 358, at 3: 96 / 109 / 149 / 247
+// (so that from 16 rows over bf16 and from 32 over 8 bits larger values would serve uneven batches better still)
+__host__ __device__ constexpr int score_ring_cost() { return 2; }
+__host__ __device__ constexpr int score_head_cost(bool q8, int rows) { return q8 && rows > 8 ? 8 : 4; }
+
 // tiles of a box of 32 or 64 rows (ring) by shifts
 __host__ __device__ __forceinline__ int score_tiles(int rows, int box) {
     return box == 64 ? (rows + 63) >> 6 : box == 32 ? (rows + 31) >> 5 : cdiv(rows, box);

@@ -216,8 +216,8 @@ struct ScoreChunk {
 
 // Tiles that begin before offset g of the line (with `upto`: at or before it); the pair of the tile that comes next
 // (upto: of the last of them), and its index.
-__device__ __forceinline__ int3 score_tiles_before(const ScoreArgs &a, const int *cum, const int *real, const int *Ts, int kvH,
-                                                int g, bool upto) {
+__host__ __device__ __forceinline__ int3 score_tiles_before(const ScoreArgs &a, const int *cum, const int *real,
+                                                            const int *Ts, int kvH, int g, bool upto) {
     const int n = seq_of(cum, a.N, g);
     const ScoreGeom sg = score_geom(Ts[n], a.plan);
     const int kh = (g - cum[n]) / sg.cost, off = g - cum[n] - kh * sg.cost;
@@ -233,8 +233,8 @@ __device__ __forceinline__ int3 score_tiles_before(const ScoreArgs &a, const int
 }
 
 // The CTAs that hold tiles of a pair: the first of them, and how many.
-__device__ __forceinline__ int2 score_parts(const ScoreArgs &a, const ScoreChunk &c, const int *cum, const int *Ts, int kvH,
-                                            int p) {
+__host__ __device__ __forceinline__ int2 score_parts(const ScoreArgs &a, const ScoreChunk &c, const int *cum,
+                                                     const int *Ts, int kvH, int p) {
     const int n = p / kvH;
     const ScoreGeom sg = score_geom(Ts[n], a.plan);
     const int last = score_begin(sg, sg.total - 1, a.plan);
@@ -247,18 +247,44 @@ __device__ __forceinline__ int2 score_parts(const ScoreArgs &a, const ScoreChunk
 // equal pieces of every head.  A head that a CTA shares costs it head_cost once more, so that pieces, which share
 // nothing across heads, are taken when they are no longer than a chunk (their own head_cost left out) or short
 // anyway; with more heads, chunks end on heads when that lengthens them by at most head_cost.
-__device__ __forceinline__ int2 score_cut(const ScoreArgs &a, int total, int cost0, bool same, int kvH) {
-    const int grid = static_cast<int>(gridDim.x), head = a.plan.head_cost, heads = a.N * kvH;
-    int chunk = max(cdiv(total, grid), a.min_chunk);
+__host__ __device__ __forceinline__ int most_of(int x, int y) { return x > y ? x : y; }
+__host__ __device__ __forceinline__ int2 score_cut(const ScoreArgs &a, int grid, int total, int cost0, bool same, int kvH) {
+    const int head = a.plan.head_cost, heads = a.N * kvH;
+    int chunk = most_of(cdiv(total, grid), a.min_chunk);
     if (same && heads <= grid) {
-        const int P = min(grid / heads, max((cost0 - head) / a.min_chunk, 1));
-        const int piece = max(cdiv(cost0 - head, P), a.plan.ring_cost);  // no shorter than a tile: each holds one
-        if (piece <= max(chunk, a.min_chunk + head)) return make_int2(piece, P);
+        const int most = most_of((cost0 - head) / a.min_chunk, 1), P = grid / heads < most ? grid / heads : most;
+        const int piece = most_of(cdiv(cost0 - head, P), a.plan.ring_cost);  // no shorter than a tile: each holds one
+        if (piece <= most_of(chunk, a.min_chunk + head)) return make_int2(piece, P);
     } else if (same && chunk >= cost0) {
         const int whole = cdiv(chunk, cost0) * cost0;
         if (whole <= chunk + head) chunk = whole;
     }
     return make_int2(chunk, 0);
+}
+
+// The tiles of CTA `cta`: of a piece of a head with geometry sg (in that head's list), or of a chunk of the line.
+__host__ __device__ __forceinline__ void score_piece(const ScoreArgs &a, const ScoreGeom &sg, int cta, ScoreChunk &c) {
+    const int at = (cta - c.p_first * c.pieces) * c.chunk;
+    c.lt = score_first(sg, at, a.plan);
+    c.ntiles = score_first(sg, at + c.chunk, a.plan) - c.lt;
+}
+__host__ __device__ __forceinline__ void score_line(const ScoreArgs &a, const int *cum, const int *real, const int *Ts,
+                                                    int kvH, int cta, ScoreChunk &c) {
+    const int begin = cta * c.chunk, end = cum[a.N] < begin + c.chunk ? cum[a.N] : begin + c.chunk;
+    if (begin >= end) return;
+    int before = 0;
+#pragma unroll 1  // one copy of the code: a small launch is paced by fetching instructions
+    for (int k = 0; k < 2; ++k) {
+        const int3 at = score_tiles_before(a, cum, real, Ts, kvH, k ? end - 1 : begin, k);
+        if (k == 0) {
+            before = at.x;
+            c.p_first = at.y;
+            c.lt = at.z;
+        } else {
+            c.ntiles = at.x - before;
+            c.p_last = at.y;
+        }
+    }
 }
 
 __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum, int *real, int *Ts, int *sflag, int tid,
@@ -275,17 +301,14 @@ __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum,
             cum[1] = sg.cost * kvH;
             real[0] = 0;
         }
-        const int2 cut = score_cut(a, sg.cost * kvH, sg.cost, true, kvH);
+        const int2 cut = score_cut(a, gridDim.x, sg.cost * kvH, sg.cost, true, kvH);
         c.chunk = cut.x;
         c.pieces = cut.y;
         __syncthreads();
         pdl_trigger();  // the next kernel may be scheduled; it waits for this one to finish
         if (c.pieces) {
             c.p_first = c.p_last = blockIdx.x / c.pieces;
-            if (c.p_first >= kvH) return c;
-            const int at = (blockIdx.x - c.p_first * c.pieces) * c.chunk;
-            c.lt = score_first(sg, at, a.plan);
-            c.ntiles = score_first(sg, at + c.chunk, a.plan) - c.lt;
+            if (c.p_first < kvH) score_piece(a, sg, blockIdx.x, c);
             return c;
         }
     } else {
@@ -324,7 +347,7 @@ __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum,
                 rcarry += __shfl_sync(0xffffffffu, r, 31);
             }
             if (lane == 0) {
-                const int2 cut = score_cut(a, carry, first / kvH, same, kvH);
+                const int2 cut = score_cut(a, gridDim.x, carry, first / kvH, same, kvH);
                 sflag[6] = cut.x;
                 sflag[7] = cut.y;
             }
@@ -334,29 +357,11 @@ __device__ __forceinline__ ScoreChunk score_chunks(const ScoreArgs &a, int *cum,
         c.pieces = sflag[7];
         if (c.pieces) {
             c.p_first = c.p_last = blockIdx.x / c.pieces;
-            if (c.p_first >= N * kvH) return c;
-            const ScoreGeom sg = score_geom(Ts[c.p_first / kvH], a.plan);
-            const int at = (blockIdx.x - c.p_first * c.pieces) * c.chunk;
-            c.lt = score_first(sg, at, a.plan);
-            c.ntiles = score_first(sg, at + c.chunk, a.plan) - c.lt;
+            if (c.p_first < N * kvH) score_piece(a, score_geom(Ts[c.p_first / kvH], a.plan), blockIdx.x, c);
             return c;
         }
     }
-    const int begin = blockIdx.x * c.chunk, end = min(cum[N], begin + c.chunk);
-    if (begin >= end) return c;
-    int before = 0;
-#pragma unroll 1  // one copy of the code: a small launch is paced by fetching instructions
-    for (int k = 0; k < 2; ++k) {
-        const int3 at = score_tiles_before(a, cum, real, Ts, kvH, k ? end - 1 : begin, k);
-        if (k == 0) {
-            before = at.x;
-            c.p_first = at.y;
-            c.lt = at.z;
-        } else {
-            c.ntiles = at.x - before;
-            c.p_last = at.y;
-        }
-    }
+    score_line(a, cum, real, Ts, kvH, blockIdx.x, c);
     return c;
 }
 

@@ -78,7 +78,7 @@ __device__ __forceinline__ bool arrive_last(int32_t *counter, int nparts, uint32
 }
 
 // index of the last sequence whose first tile is <= gt
-__device__ __forceinline__ int seq_of(const int *cum, int N, int gt) {
+__host__ __device__ __forceinline__ int seq_of(const int *cum, int N, int gt) {
     int lo = 0, hi = N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
