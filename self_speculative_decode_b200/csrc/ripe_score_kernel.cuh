@@ -36,9 +36,10 @@
 //   * A masked value never reaches a sum: stale ring rows or later draft rows may hold NaN or infinity.
 //
 // Measured (one B200, 8 sequences x 32768 keys, 8 kv heads x 128; 6456 GB/s is the measured copy): over the 8-bit
-// region 88 us at 4 rows a kv head (0.94 of it), 102 us at 16 (0.82), 160 to 166 us at 32 (0.50 to 0.52: paced by instructions, 3.25 warps a
-// scheduler; 178 us with 16 rows and 32 keys a warp, 180 us with 32 rows, 16 keys and all of head_dim a warp, 194 us with
-// two groups instead of three); capped, over bf16, 193 to 200 us at 32 rows (0.83 to 0.86).
+// region 87 us at 4 rows a kv head (0.96 of it), 102 us at 16 (0.82), 160 to 166 us at 32 (0.50 to 0.52: paced by instructions,
+// 3.25 warps a scheduler; 178 us with 16 rows and 32 keys a warp, 180 us with 32 rows, 16 keys and all of head_dim a warp,
+// 194 us with two groups instead of three), 297 us at 64; capped, over bf16, 193 to 200 us at 32 rows (0.83 to 0.86), 209 us
+// with a cap from kCapSeries on.
 #pragma once
 
 #include <cuda_fp16.h>
