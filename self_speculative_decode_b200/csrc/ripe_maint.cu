@@ -26,7 +26,7 @@ __device__ __forceinline__ size_t deep_row(int layer, int n, int kh, int t, int 
 // k, v [N][B][kvH][d] -> ring plane r, slot (T_n + j) mod S.
 __global__ void ripe_append_kernel(uint4 *__restrict__ Kw, uint4 *__restrict__ Vw,
                                    const uint4 *__restrict__ k, const uint4 *__restrict__ v,
-                                   const int32_t *__restrict__ T, uint32_t *err, int N, int B, int kvH,
+                                   const int32_t *T, uint32_t *err, int N, int B, int kvH,
                                    int d8, int R, int S, int layer, int r, int max_T, int early) {
     // The next launch may start at once: a verify launch reads nothing this kernel writes before
     // its own wait, which returns only after this kernel (and so its predecessor) has completed.
@@ -45,16 +45,18 @@ __global__ void ripe_append_kernel(uint4 *__restrict__ Kw, uint4 *__restrict__ V
         rest /= kvH;
         const int j = static_cast<int>(rest % B);
         const int n = static_cast<int>(rest / B);
-        const int Tn = __ldcg(T + n);
+        // not the read-only path: a rotation launched before this (ripe_rotate_block) may have been writing them.
+        // All three loads before anything else, so that they overlap
+        const uint4 kx = __ldcg(k + idx), vx = __ldcg(v + idx);
+        const int Tn = T[n];
         if (Tn + B > max_T) {
             if (j == 0 && kh == 0 && c8 == 0) atomicOr(err, RIPE_DEVERR_CAPACITY);
             continue;
         }
         const int slot = (Tn + j) % S;
         const size_t dst = ring_row(layer, n, r, kh, slot, N, R, kvH, S) * d8 + c8;
-        // not the read-only path: a rotation launched before this (ripe_rotate_block) may have been writing them
-        Kw[dst] = __ldcg(k + idx);
-        Vw[dst] = __ldcg(v + idx);
+        Kw[dst] = kx;
+        Vw[dst] = vx;
     }
 }
 
@@ -80,14 +82,14 @@ int launch_append(ripe_cache *c, int layer, int r, int B, const void *k, const v
 // reused by later positions).  One CTA row per (layer, sequence).
 __global__ void ripe_evict_kernel(uint4 *__restrict__ Kd, uint4 *__restrict__ Vd,
                                   const uint4 *__restrict__ Kw, const uint4 *__restrict__ Vw,
-                                  const int32_t *__restrict__ T, const HostIntArray acc_h,
+                                  const int32_t *T, const HostIntArray acc_h,
                                   const int32_t *acc_d, uint32_t *err, int N, int B, int kvH, int d8,
                                   int R, int S, int W, int deep_rows, int max_T) {
     pdl_wait();
     pdl_trigger();
     const int layer = blockIdx.x / N;
     const int n = blockIdx.x - layer * N;
-    const int Tn = __ldcg(T + n);
+    const int Tn = T[n];
     const int a = accepted(acc_h, acc_d, n, B, Tn, max_T, nullptr);
     const int lo = Tn - W > 0 ? Tn - W : 0;
     const int hi = Tn + a - W > 0 ? Tn + a - W : 0;
@@ -104,8 +106,9 @@ __global__ void ripe_evict_kernel(uint4 *__restrict__ Kd, uint4 *__restrict__ Vd
         }
         const size_t src = ring_row(layer, n, R - 1, kh, t % S, N, R, kvH, S) * d8 + c8;
         const size_t dst = deep_row(layer, n, kh, t, N, kvH, deep_rows) * d8 + c8;
-        Kd[dst] = __ldcg(Kw + src);
-        Vd[dst] = __ldcg(Vw + src);
+        const uint4 kx = __ldcg(Kw + src), vx = __ldcg(Vw + src);
+        Kd[dst] = kx;
+        Vd[dst] = vx;
     }
 }
 

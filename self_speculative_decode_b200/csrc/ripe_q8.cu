@@ -190,7 +190,7 @@ __global__ void ripe_q8_load_ring_kernel(uint4 *__restrict__ Kw, uint4 *__restri
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4)
 ripe_q8_evict_kernel(uint8_t *__restrict__ rec, const uint4 *__restrict__ Kw, const uint4 *__restrict__ Vw,
-                     const int32_t *__restrict__ T, const HostIntArray acc_h, const int32_t *acc_d, int L, int N,
+                     const int32_t *T, const HostIntArray acc_h, const int32_t *acc_d, int L, int N,
                      int B, int kvH, int R, int S, int W, int rec_blocks, int max_T) {
     __shared__ __align__(16) uint8_t buf[128 * D];
     __shared__ uint32_t red[16];
@@ -199,7 +199,7 @@ ripe_q8_evict_kernel(uint8_t *__restrict__ rec, const uint4 *__restrict__ Kw, co
     const int items = L * N * kvH;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
         const int kh = it % kvH, n = (it / kvH) % N, layer = it / kvH / N;
-        const int Tn = __ldcg(T + n), p0 = q8_end(Tn, W);
+        const int Tn = T[n], p0 = q8_end(Tn, W);
         const int a = accepted(acc_h, acc_d, n, B, Tn, max_T, nullptr);  // (the length update reports)
         if (q8_end(Tn + a, W) == p0 || p0 / kQ8Block >= rec_blocks) continue;
         const size_t row0 = ring_row(layer, n, R - 1, kh, 0, N, R, kvH, S);

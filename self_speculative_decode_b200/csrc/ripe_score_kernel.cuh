@@ -581,7 +581,7 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
             const uint32_t *qp = reinterpret_cast<const uint32_t *>(
                 a.q + ((static_cast<size_t>(p / kvH) * a.qB + j) * a.Hq + h * a.g + hg) * D);
 #pragma unroll
-            for (int u = 0; u < QW; ++u) qw[r][u] = have && u * 32 + lane < D / 2 ? __ldcg(qp + u * 32 + lane) : 0u;
+            for (int u = 0; u < QW; ++u) qw[r][u] = have && u * 32 + lane < D / 2 ? qp[u * 32 + lane] : 0u;
         }
     };
     auto stage_q = [&](int p) {

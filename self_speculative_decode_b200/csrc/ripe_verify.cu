@@ -444,9 +444,10 @@ ripe_verify_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_consta
             }
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-                // not the read-only path: the launch before this one may have been writing them (ripe_rope.cu)
-                qb[ks][nq][0] = qp ? __ldcg(qp + 8 * ks + c4) : 0u;
-                qb[ks][nq][1] = qp ? __ldcg(qp + 8 * ks + 4 + c4) : 0u;
+                // not the read-only path: the launch before this one may have been writing them (ripe_rope.cu).  Not
+                // past L1 either: the warps share rows, and the Huginn-shaped step would take 4 % longer
+                qb[ks][nq][0] = qp ? qp[8 * ks + c4] : 0u;
+                qb[ks][nq][1] = qp ? qp[8 * ks + 4 + c4] : 0u;
             }
         }
     };

@@ -723,7 +723,7 @@ ripe_verify_tc_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_con
                         for (int c = 0; c < D / 8; ++c) {
                             const int box = c >> 2, ch = (c & 3) ^ ((mrow >> 1) & 3);
                             // not the read-only path, as ripe_verify.cu
-                            *reinterpret_cast<uint4 *>(qs + box * kBoxBytes + mrow * 64 + ch * 16) = __ldcg(src + c);
+                            *reinterpret_cast<uint4 *>(qs + box * kBoxBytes + mrow * 64 + ch * 16) = src[c];
                         }
                     }
                     fence_async_smem();
