@@ -21,10 +21,11 @@
  *     Host pointers are read before the call returns.
  *   - `stream` is a cudaStream_t (NULL = legacy default stream).  All device
  *     work is enqueued on it; calls return after enqueueing.
- *   - bf16 tensors are IEEE bfloat16, contiguous, row-major in the order given.  Keys and values (and exports of
- *     them) are 16-byte aligned; q, out, lse and device int32 arrays 4-byte aligned, q 16-byte aligned for more than 8
- *     query rows per kv head while RIPE_CONSUMER_TC is selected; what the rotating calls ask is said there.
- *     RIPE_EINVAL otherwise.
+ *   - bf16 tensors are IEEE bfloat16, contiguous, row-major in the order given.  Keys and values
+ *     (and the exports of a bf16 cache) are 16-byte aligned, q, out, lse and device int32 arrays
+ *     4-byte aligned; q is 16-byte aligned for more than 8 query rows per kv head while
+ *     RIPE_CONSUMER_TC is selected.  What the rotating calls ask is said there.  RIPE_EINVAL
+ *     otherwise.
  *   - Argument and state errors are detected on the host before anything is
  *     enqueued and leave the cache unchanged.  A failed launch returns
  *     RIPE_ECUDA.  Faults detected by a kernel (a wait that gave up, a block

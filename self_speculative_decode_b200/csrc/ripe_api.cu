@@ -559,7 +559,7 @@ int ripe_cache_export(ripe_cache_t *c, int n, int layer, void *k_out, void *v_ou
                       void *stream) {
     const NvtxRange nvtx_range("ripe_cache_export");
     if (!c || !k_out || !v_out || !plane_present || n < 0 || n >= c->N || layer < 0 || layer >= c->L ||
-        !aligned_to(16, k_out, v_out))
+        !aligned_to(c->kv_bits == 8 ? 2 : 16, k_out, v_out))
         return RIPE_EINVAL;
     if (!c->synced) return RIPE_ESTATE;
     DeviceGuard g(c->device);

@@ -1112,9 +1112,10 @@ ripe_score_kernel(const __grid_constant__ CUtensorMap tmKd, const __grid_constan
 
     // moves a column's reference up by `up`; its sums are worth 2^lg of what they were then
     auto move_ref = [&](int nq, int e, float up, float lg, float (&x)[C::SB][NQT][4]) {
-        const float al = exp2f(fmaxf(lg, -100.f));  // (O is as good as 0 then)
-        l_lse[nq][e] *= al;
-        if (lg < -100.f) l_lse[nq][e] *= exp2f(lg + 100.f);
+        const bool far = lg < -100.f;  // what O holds is 2^-100 of what comes then; the normaliser may still hold more
+        const float al = far ? 0.f : exp2f(lg);
+        l_lse[nq][e] *= far ? exp2f(0.5f * lg) : al;
+        if (far) l_lse[nq][e] *= exp2f(0.5f * lg);
         if constexpr (C::WIDE) {
             const int col = 8 * nq + 2 * c4 + e;
             if (g4 == 0) gfix[warp * C::NQ + col] *= al;

@@ -329,3 +329,20 @@ def test_slopes_at_the_end_of_fp32(cuda_device):
                 got = out[0, j, h].float().cpu().numpy()
                 assert (abs(got - v) <= 2.0 ** -7 * abs(v)).all()
         p.close()
+
+
+def test_a_column_of_zeros_beside_values_of_other_blocks(cuda_device):
+    """What a block of tiny values adds to a column that a later, large block leaves at zero is not blown up."""
+    for Hq, B in ((2, 1), (4, 4), (8, 4)):
+        p = Pair(1, Hq, 1, 64, 1, 8, 400, B, seed=6)
+        rng = np.random.default_rng(0)
+        for b, size in enumerate((1e-24, 1e-24, 1e24, 1e24, 1e-24, 1e24)):
+            x = rng.standard_normal((1, 1, 64, 64)).astype(np.float32) * np.float32(size)
+            if size > 1:
+                x[..., ::2] = 0
+            p.planes[0][0][1][:, :, 64 * b: 64 * b + 64] = synth.f32_to_bf16_bits(x)
+        p.planes[0][0][1][:, :, 384:] = synth.f32_to_bf16_bits(np.zeros((1, 1, p.max_T - 384, 64), np.float32))
+        p.load().append(B)
+        out = p.gpu.verify_attn(0, 0, bits_dev(p.queries(B)))
+        assert (out[..., ::2].abs() <= 1e-23).all() and (out[..., 1::2].abs() > 1e18).any()
+        p.close()
